@@ -5,6 +5,12 @@
  *   tq_store            fused quantising store of new K/V tokens into a paged cache
  *   tq_decode_attention split-K decode attention read straight from that cache
  *   tq_dequant          cached slots back to K/V in the original space
+ *   tq_decode_attention_scored   the decode with capped or biased scores, a
+ *                       window, a prefix and document starts
+ *   tq_decode_attention_weights  the same, adding each token's attention weight
+ *                       to a running sum
+ *   tq_evict_select, tq_evict_compact   which tokens a kv head keeps by those
+ *                       sums, and the move of their slots, in place
  *   tq_build_codebook, tq_make_signs, tq_get_layout   host set-up
  *
  * Cache layout (one combined K+V slot per (block, token, kv head), no leading
@@ -297,6 +303,118 @@ int tq_decode_attention_noalloc(int preset, int head_dim, int batch, int num_q_h
                                 float softmax_scale, int num_splits,
                                 const int8_t* signs, const float* centroids,
                                 void* out, int out_dtype, float* lse, void* stream);
+
+/* Score modifiers of a decode.  For the token t of a sequence of L tokens and
+ * query head hq, with x = softmax_scale * <q, k_t> as in tq_decode_attention:
+ *   softcap > 0:      x = softcap * tanh(x / softcap);
+ *   alibi_slopes:     then x -= alibi_slopes[hq] * (L - 1 - t);
+ *   window, prefix, doc_start: with lo = max(doc_start[b], 0) (0 without
+ *     doc_start) only tokens lo <= t < L with window == 0, t >= L - window or
+ *     t < lo + prefix are visible.  The others take no part in the softmax; pages
+ *     with no visible token are neither looked up nor read, so their table
+ *     entries may be stale.  prefix counts only beside a window.
+ * A sequence with no visible token gives o = 0 and lse = -inf.  The page
+ * "vllm.v1.attention.backends.turboquant_attn" names the sliding window and the
+ * first tokens (sinks) as masks of its decode; its other masks and the cap have
+ * no counterpart on the pages.
+ * alibi_slopes: device float[num_q_heads] or NULL; doc_start: device
+ * int32[batch] or NULL; softcap >= 0 and finite, window >= 0, prefix >= 0. */
+typedef struct {
+    float softcap;
+    int window;
+    int prefix;
+    const float* alibi_slopes;
+    const int32_t* doc_start;
+} tq_score_mods;
+
+/* tq_decode_attention with score modifiers; mods NULL (or all zero) is
+ * tq_decode_attention exactly.  num_splits = 0 picks as tq_decode_pick_splits
+ * does for the longest visible length, 32 * T tokens with T the smaller of
+ * ceil(max_seq_len / 32) and, with a window, window / 32 + 2 (+ prefix / 32 + 2
+ * when prefix > 0), but at most max_seq_len.  The splits share the 32-token
+ * tiles that hold visible tokens.  Other arguments, results, errors and
+ * supported shapes as tq_decode_attention; TQ_ERR_INVALID_ARG for modifiers out
+ * of range or max_seq_len above 2^30. */
+int tq_decode_attention_scored(int preset, int head_dim, int batch, int num_q_heads,
+                               int num_kv_heads, int block_size, int q_dtype, const void* query,
+                               const uint8_t* kv_cache, long long num_blocks,
+                               const int32_t* block_table, int block_table_stride,
+                               const int32_t* seq_lens, int max_seq_len, float softmax_scale,
+                               int num_splits, const int8_t* signs, const float* centroids,
+                               void* out, int out_dtype, float* lse, void* workspace,
+                               size_t workspace_bytes, const tq_score_mods* mods, void* stream);
+
+/* Bytes of caller-owned workspace of tq_decode_attention_weights: the split
+ * partials, an lse per query head and the scores of every listed token, about
+ * 4 * num_q_heads bytes per visible token.  0 for sizes out of range. */
+size_t tq_decode_weights_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
+                                         int num_splits, int head_dim, int max_seq_len,
+                                         int window, int prefix);
+
+/* tq_decode_attention_scored that also adds up attention weights: for every
+ * visible token t of sequence b and kv head h
+ *   acc[b*acc_stride_seq + h*acc_stride_head + t] += sum_g exp(x_g(t) - lse_g)
+ * over the query heads g of h (x with its modifiers, lse the row's; fp32).
+ * The sums of other tokens, and of entries at or past seq_lens[b], are left as
+ * they are.  The cache is read once.  mods may be NULL.
+ * acc: device float; rows of max_seq_len elements that must not overlap
+ * (TQ_ERR_INVALID_ARG).  Rows go by batch index: several queries of one
+ * sequence in a call add to rows of their own.
+ * max_seq_len binds here: a sequence longer than it comes out NaN (output and
+ * lse) and its sums stay.  A sequence whose lse is NaN (a page outside the
+ * cache) gets NaN sums at its visible tokens.
+ * workspace: >= tq_decode_weights_workspace_bytes for the split count used
+ * (TQ_ERR_WORKSPACE), 16-byte aligned; calls that overlap on the GPU need one
+ * each. */
+int tq_decode_attention_weights(int preset, int head_dim, int batch, int num_q_heads,
+                                int num_kv_heads, int block_size, int q_dtype, const void* query,
+                                const uint8_t* kv_cache, long long num_blocks,
+                                const int32_t* block_table, int block_table_stride,
+                                const int32_t* seq_lens, int max_seq_len, float softmax_scale,
+                                int num_splits, const int8_t* signs, const float* centroids,
+                                void* out, int out_dtype, float* lse, void* workspace,
+                                size_t workspace_bytes, const tq_score_mods* mods, float* acc,
+                                long long acc_stride_seq, long long acc_stride_head, void* stream);
+
+/* Which tokens each kv head keeps, by the running sums of
+ * tq_decode_attention_weights.  A sequence of L > budget tokens keeps budget of
+ * them per kv head: its first `prefix`, its newest `recent`, and of the rest
+ * those with the largest sums, equal sums in order of the lower index (-0
+ * counts as 0; a NaN is above every number).  A sequence of at most budget
+ * tokens keeps all.
+ * acc: device float, strides as there, read only.  keep: device
+ * int32[batch][num_kv_heads][budget], the kept token indices ascending, -1
+ * past a sequence of fewer tokens.  new_lens: device int32[batch], min(L,
+ * budget).  A sequence longer than max_seq_len is a caller error: nothing of it
+ * is read, its keep entries are -1 and its new_lens entry is L.
+ * budget >= 1, prefix + recent <= budget, max_seq_len <= 2^30.  Returns TQ_OK, TQ_ERR_INVALID_ARG
+ * or TQ_ERR_CUDA. */
+int tq_evict_select(int batch, int num_kv_heads, const float* acc, long long acc_stride_seq,
+                    long long acc_stride_head, const int32_t* seq_lens, int max_seq_len, int budget,
+                    int prefix, int recent, int32_t* keep, int32_t* new_lens, void* stream);
+
+/* The kept slots to the front of their sequences, in place: for every sequence
+ * of L > budget tokens and kv head, slot i (i < budget) becomes what slot
+ * keep[b][h][i] was, byte for byte, and with acc (may be NULL) its running sum
+ * likewise; the sums of tokens budget .. L - 1 become 0.  Sequences of at most
+ * budget tokens, and of more than max_seq_len, are left alone.  Slots from
+ * budget on keep their bytes; the pages that hold only such slots may be freed.
+ * Afterwards the sequence has budget tokens (the new_lens of tq_evict_select):
+ * distances of alibi_slopes, windows and document starts count in the shortened
+ * sequence.
+ * keep: as tq_evict_select writes it for these seq_lens (the lengths before the
+ * eviction): ascending, so keep[i] >= i.  An entry outside [0, L), or one whose
+ * page or whose destination's page lies outside [0, num_blocks), moves nothing;
+ * entries that do not ascend leave unspecified contents in that sequence's own
+ * slots.  Pages must belong to one sequence each (a shared page would be moved
+ * under the other's feet): copy them first.
+ * Layouts (AoS and TQ_LAYOUT_SOA), block sizes and head_dim as tq_store;
+ * max_seq_len <= 2^30. */
+int tq_evict_compact(int preset, int head_dim, int batch, int num_kv_heads, int block_size,
+                     uint8_t* kv_cache, long long num_blocks, const int32_t* block_table,
+                     int block_table_stride, const int32_t* keep, int budget,
+                     const int32_t* seq_lens, int max_seq_len, float* acc,
+                     long long acc_stride_seq, long long acc_stride_head, void* stream);
 
 /* Test entry point for the bounded waits of the tensor-core stage 1; the
  * pages have no counterpart.  Runs tq_decode_attention (num_splits as there)

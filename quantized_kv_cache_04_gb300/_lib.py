@@ -36,6 +36,11 @@ class TQLayout(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+class TQScoreMods(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int), ("prefix", ctypes.c_int),
+                ("alibi_slopes", ctypes.c_void_p), ("doc_start", ctypes.c_void_p)]
+
+
 class TQError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn}: {tq_status_string(status)} ({status})")
@@ -79,6 +84,18 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                                                _c_vp, _c_sz, ctypes.c_float, _c_vp])
     L.tq_dequant.argtypes = ([_c_int] * 5 + [_c_vp, _c_ll, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_int,
                                              _c_ll, _c_ll, _c_vp])
+    L.tq_decode_attention_scored.argtypes = ([_c_int] * 7 + [_c_vp, _c_vp, _c_ll, _c_vp, _c_int,
+                                                             _c_vp, _c_int, ctypes.c_float, _c_int,
+                                                             _c_vp, _c_vp, _c_vp, _c_int, _c_vp,
+                                                             _c_vp, _c_sz, ctypes.POINTER(TQScoreMods), _c_vp])
+    L.tq_decode_attention_weights.argtypes = (L.tq_decode_attention_scored.argtypes[:-1]
+                                              + [_c_vp, _c_ll, _c_ll, _c_vp])
+    L.tq_decode_weights_workspace_bytes.argtypes = [_c_int] * 8
+    L.tq_decode_weights_workspace_bytes.restype = _c_sz
+    L.tq_evict_select.argtypes = ([_c_int] * 2 + [_c_vp, _c_ll, _c_ll, _c_vp] + [_c_int] * 4
+                                  + [_c_vp] * 3)
+    L.tq_evict_compact.argtypes = ([_c_int] * 5 + [_c_vp, _c_ll, _c_vp, _c_int, _c_vp, _c_int, _c_vp,
+                                                   _c_int, _c_vp, _c_ll, _c_ll, _c_vp])
     L.tq_status_string.argtypes = [_c_int]
     L.tq_status_string.restype = ctypes.c_char_p
     L.tq_version.restype = _c_int
@@ -163,6 +180,34 @@ def tq_dequant(*args) -> int:
     return load().tq_dequant(*args)
 
 
+def tq_decode_attention_scored(*args) -> int:
+    """Raw C call; arguments exactly as in include/tq.h.  Returns the status."""
+    return load().tq_decode_attention_scored(*args)
+
+
+def tq_decode_attention_weights(*args) -> int:
+    """Raw C call; arguments exactly as in include/tq.h.  Returns the status."""
+    return load().tq_decode_attention_weights(*args)
+
+
+def tq_decode_weights_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, num_splits: int,
+                                      head_dim: int, max_seq_len: int, window: int = 0,
+                                      prefix: int = 0) -> int:
+    return int(load().tq_decode_weights_workspace_bytes(
+        int(batch), int(num_q_heads), int(num_kv_heads), int(num_splits), int(head_dim),
+        int(max_seq_len), int(window), int(prefix)))
+
+
+def tq_evict_select(*args) -> int:
+    """Raw C call; arguments exactly as in include/tq.h.  Returns the status."""
+    return load().tq_evict_select(*args)
+
+
+def tq_evict_compact(*args) -> int:
+    """Raw C call; arguments exactly as in include/tq.h.  Returns the status."""
+    return load().tq_evict_compact(*args)
+
+
 # ------------------------------------------------------------------ torch helpers
 def _dtype_code(t) -> int:
     import torch
@@ -230,6 +275,195 @@ def decode_attention(preset: int, query, kv_cache, block_table, seq_lens, max_se
     rc = tq_decode_attention(*args, _stream_ptr(stream))
     if rc:
         raise TQError("tq_decode_attention", rc)
+
+
+def _need(ok: bool, fn: str, what: str) -> None:
+    if not ok:
+        raise ValueError(f"{fn}: {what}")
+
+
+def _on(t, device, dtypes, shape, fn: str, name: str, contiguous: bool = True) -> None:
+    """t is a tensor of one of `dtypes` on `device` with this shape (None: any size)."""
+    import torch
+    _need(isinstance(t, torch.Tensor), fn, f"{name} is not a tensor")
+    _need(t.device == device and t.is_cuda, fn, f"{name} is on {t.device}, not on the call's GPU {device}")
+    _need(t.dtype in dtypes, fn, f"{name} has dtype {t.dtype}")
+    _need(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)), fn,
+          f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    _need(not contiguous or t.is_contiguous(), fn, f"{name} is not contiguous")
+
+
+def _table_and_lens(fn, device, block_table, seq_lens, B: int):
+    import torch
+    _on(block_table, device, (torch.int32,), (B, None), fn, "block_table", contiguous=False)
+    _need(block_table.shape[1] <= 1 or block_table.stride(1) == 1, fn, "block_table rows are not contiguous")
+    _on(seq_lens, device, (torch.int32,), (B,), fn, "seq_lens")
+
+
+def _acc_strides(acc):
+    """Row strides of running sums (B, Hk, T); those of single rows, which are never used, made plain."""
+    B, Hk, T = acc.shape
+    sh = acc.stride(1) if Hk > 1 else T
+    return (acc.stride(0) if B > 1 else Hk * sh), sh
+
+
+class _Device:
+    """The tensors' GPU as the current one, and the stream of a call on it."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard, self.device, self.stream = torch.cuda.device(device), device, stream
+
+    def __enter__(self):
+        import torch
+        self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _listed_len(max_seq_len: int, window: int, prefix: int) -> int:
+    """The longest visible length num_splits = 0 is picked for (include/tq.h)."""
+    if window <= 0:
+        return max_seq_len
+    some = window // 32 + 2 + (prefix // 32 + 2 if prefix > 0 else 0)
+    return min(max_seq_len, 32 * min((max_seq_len + 31) // 32, some))
+
+
+def scored_workspace_bytes(preset: int, batch: int, num_q_heads: int, num_kv_heads: int, max_seq_len: int,
+                           window: int = 0, prefix: int = 0, weights: bool = False, num_splits: int = 0,
+                           head_dim: int = 128) -> int:
+    """Workspace bytes of decode_attention_scored, or with `weights` of decode_attention_weights, for the
+    split count given or the one the library picks."""
+    S = int(num_splits) or tq_decode_pick_splits(preset, head_dim, batch, num_q_heads, num_kv_heads,
+                                                 _listed_len(int(max_seq_len), int(window), int(prefix)))
+    if weights:
+        n = tq_decode_weights_workspace_bytes(batch, num_q_heads, num_kv_heads, S, head_dim, max_seq_len,
+                                              window, prefix)
+    else:
+        n = tq_decode_workspace_bytes(batch, num_q_heads, S, head_dim)
+    return max(16, n)
+
+
+def _scored_args(fn, preset, query, kv_cache, block_table, seq_lens, max_seq_len, num_kv_heads, block_size, signs,
+                 centroids, out, lse, workspace, num_splits, softmax_scale, softcap, alibi_slopes, window,
+                 prefix, doc_start):
+    import torch
+    dev = query.device
+    _on(query, dev, (torch.float16, torch.bfloat16), (None, None, None), fn, "query")
+    B, Hq, D = query.shape
+    _on(out, dev, (torch.float16, torch.bfloat16, torch.float32), (B, Hq, D), fn, "out")
+    if lse is not None:
+        _on(lse, dev, (torch.float32,), (B, Hq), fn, "lse")
+    _table_and_lens(fn, dev, block_table, seq_lens, B)
+    lay = tq_get_layout(int(preset), D)
+    _on(kv_cache, dev, (torch.uint8,), (None, int(block_size), int(num_kv_heads), lay["slot_size_aligned"]), fn,
+        "kv_cache")
+    if not lay["key_fp8"]:
+        _on(signs, dev, (torch.int8,), (D,), fn, "signs")
+        _on(centroids, dev, (torch.float32,), (lay["n_centroids"],), fn, "centroids")
+    _need(workspace.device == dev and workspace.is_contiguous(), fn, "workspace is not contiguous memory of the call's GPU")
+    if alibi_slopes is not None:
+        _on(alibi_slopes, dev, (torch.float32,), (Hq,), fn, "alibi_slopes")
+    if doc_start is not None:
+        _on(doc_start, dev, (torch.int32,), (B,), fn, "doc_start")
+    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
+    mods = TQScoreMods(float(softcap), int(window), int(prefix), _ptr(alibi_slopes) or None, _ptr(doc_start) or None)
+    return (int(preset), D, B, Hq, int(num_kv_heads), int(block_size), _dtype_code(query), _ptr(query),
+            _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table), block_table.stride(0), _ptr(seq_lens),
+            int(max_seq_len), scale, int(num_splits), _ptr(signs), _ptr(centroids), _ptr(out),
+            _dtype_code(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            ctypes.byref(mods))
+
+
+def decode_attention_scored(preset: int, query, kv_cache, block_table, seq_lens, max_seq_len: int,
+                            num_kv_heads: int, block_size: int, signs, centroids, out, lse, workspace,
+                            num_splits: int = 0, softmax_scale: float | None = None, stream=None, *,
+                            softcap: float = 0.0, alibi_slopes=None, window: int = 0, prefix: int = 0,
+                            doc_start=None) -> None:
+    """tq_decode_attention_scored on torch tensors.  query (B, Hq, D) contiguous; alibi_slopes float32 (Hq,);
+    doc_start int32 (B,); workspace as scored_workspace_bytes says."""
+    fn = "decode_attention_scored"
+    args = _scored_args(fn, preset, query, kv_cache, block_table, seq_lens, max_seq_len, num_kv_heads, block_size,
+                        signs, centroids, out, lse, workspace, num_splits, softmax_scale, softcap, alibi_slopes,
+                        window, prefix, doc_start)
+    with _Device(query.device, stream) as st:
+        rc = tq_decode_attention_scored(*args, st)
+    if rc:
+        raise TQError("tq_decode_attention_scored", rc)
+
+
+def decode_attention_weights(preset: int, query, kv_cache, block_table, seq_lens, max_seq_len: int,
+                             num_kv_heads: int, block_size: int, signs, centroids, out, lse, workspace, acc,
+                             num_splits: int = 0, softmax_scale: float | None = None, stream=None, *,
+                             softcap: float = 0.0, alibi_slopes=None, window: int = 0, prefix: int = 0,
+                             doc_start=None) -> None:
+    """tq_decode_attention_weights on torch tensors: decode_attention_scored that also adds every visible
+    token's attention weight to acc, float32 (B, Hk, T) with T >= max_seq_len and contiguous rows.
+    lse may be None; workspace as scored_workspace_bytes(..., weights=True) says."""
+    import torch
+    fn = "decode_attention_weights"
+    args = _scored_args(fn, preset, query, kv_cache, block_table, seq_lens, max_seq_len, num_kv_heads, block_size,
+                        signs, centroids, out, lse, workspace, num_splits, softmax_scale, softcap, alibi_slopes,
+                        window, prefix, doc_start)
+    _on(acc, query.device, (torch.float32,), (query.shape[0], int(num_kv_heads), None), fn, "acc", contiguous=False)
+    _need(acc.shape[2] >= int(max_seq_len), fn, f"acc rows hold {acc.shape[2]} tokens, max_seq_len is {max_seq_len}")
+    _need(acc.shape[2] <= 1 or acc.stride(2) == 1, fn, "acc rows are not contiguous")
+    with _Device(query.device, stream) as st:
+        rc = tq_decode_attention_weights(*args, _ptr(acc), *_acc_strides(acc), st)
+    if rc:
+        raise TQError("tq_decode_attention_weights", rc)
+
+
+def evict_select(acc, seq_lens, max_seq_len: int, budget: int, keep, new_lens, prefix: int = 0, recent: int = 0,
+                 stream=None) -> None:
+    """tq_evict_select on torch tensors: acc float32 (B, Hk, T), T >= max_seq_len, contiguous rows; keep int32
+    (B, Hk, budget) and new_lens int32 (B,) are written."""
+    import torch
+    fn = "evict_select"
+    dev = acc.device
+    _on(acc, dev, (torch.float32,), (None, None, None), fn, "acc", contiguous=False)
+    B, Hk, T = acc.shape
+    _need(T >= int(max_seq_len), fn, f"acc rows hold {T} tokens, max_seq_len is {max_seq_len}")
+    _need(T <= 1 or acc.stride(2) == 1, fn, "acc rows are not contiguous")
+    _on(seq_lens, dev, (torch.int32,), (B,), fn, "seq_lens")
+    _on(keep, dev, (torch.int32,), (B, Hk, int(budget)), fn, "keep")
+    _on(new_lens, dev, (torch.int32,), (B,), fn, "new_lens")
+    with _Device(dev, stream) as st:
+        rc = tq_evict_select(B, Hk, _ptr(acc), *_acc_strides(acc), _ptr(seq_lens), int(max_seq_len), int(budget),
+                             int(prefix), int(recent), _ptr(keep), _ptr(new_lens), st)
+    if rc:
+        raise TQError("tq_evict_select", rc)
+
+
+def evict_compact(preset: int, keep, seq_lens, kv_cache, block_table, num_kv_heads: int, block_size: int, acc=None,
+                  stream=None) -> None:
+    """tq_evict_compact on torch tensors: the slots keep (int32 (B, Hk, budget)) names move to the front of their
+    sequences in kv_cache, and the running sums acc (float32 (B, Hk, T)) with them.  seq_lens: the lengths
+    before the eviction; sequences longer than the table or acc covers are left alone."""
+    import torch
+    fn = "evict_compact"
+    dev = kv_cache.device
+    _on(keep, dev, (torch.int32,), (None, int(num_kv_heads), None), fn, "keep")
+    B, Hk, budget = keep.shape
+    _table_and_lens(fn, dev, block_table, seq_lens, B)
+    _need(B <= 1 or block_table.stride(0) >= block_table.shape[1], fn, "block_table rows overlap")
+    slot = tq_get_layout(int(preset), 128)["slot_size_aligned"]
+    _on(kv_cache, dev, (torch.uint8,), (None, int(block_size), Hk, slot), fn, "kv_cache")
+    max_len = min(block_table.shape[1] * int(block_size), 1 << 30)
+    strides = (0, 0)
+    if acc is not None:
+        _on(acc, dev, (torch.float32,), (B, Hk, None), fn, "acc", contiguous=False)
+        _need(acc.shape[2] <= 1 or acc.stride(2) == 1, fn, "acc rows are not contiguous")
+        max_len, strides = min(max_len, acc.shape[2]), _acc_strides(acc)
+    with _Device(dev, stream) as st:
+        rc = tq_evict_compact(int(preset), 128, B, Hk, int(block_size), _ptr(kv_cache), kv_cache.shape[0],
+                              _ptr(block_table), block_table.stride(0), _ptr(keep), budget, _ptr(seq_lens), max_len,
+                              _ptr(acc), *strides, st)
+    if rc:
+        raise TQError("tq_evict_compact", rc)
 
 
 TQ_NOALLOC_SCRATCH_BYTES = 16 << 20

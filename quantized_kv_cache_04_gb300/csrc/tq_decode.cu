@@ -7,15 +7,12 @@
 // shared mid_o / lse scratch); "turboquant-plus.md", "weight pre-rotation"
 // note (<Q H, H K> = <Q, K>, so q is rotated once and keys stay rotated).
 //
-// This file holds the host entry point, stage 2 (the log-sum-exp merge) and
-// the CUDA-core stage 1 used for shapes the tensor-core stage 1
-// (tq_decode_mma.cu) does not serve: one CTA per (split, kv head, sequence),
-// four warps striding over the split's tokens, 4 coordinates per lane, fp32
-// scores and online softmax, partials merged across warps in shared memory.
-#include "tq.h"
-#include "tq_device.cuh"
-#include "tq_internal.h"
+// This file holds the host entry points, stage 2 (the log-sum-exp merge) and
+// the plain instantiations of the CUDA-core stage 1 (tq_decode_cores.cuh),
+// used for shapes the tensor-core stage 1 (tq_decode_mma.cu) does not serve.
+#include "tq_decode_cores.cuh"
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 #include <vector>
@@ -23,201 +20,6 @@
 namespace tq {
 
 namespace {
-
-struct DecodeArgs {
-    const void* query;
-    const uint8_t* cache;
-    long long num_blocks;
-    const int32_t* block_table;
-    int bt_stride;
-    const int32_t* seq_lens;
-    float scale;
-    int num_splits;
-    const int8_t* signs;
-    const float* centroids;
-    float* mid;          // (B, Hq, S, D+1)
-    void* out;
-    float* lse;
-    int B, Hq, Hk, G, bs;
-    float vthr;          // sparse V: rows with p <= vthr skip the value sum (0: off)
-    SlotGeom g;
-};
-
-constexpr int kWarps = 4;
-
-// Codes 4*lane .. 4*lane+3 of a packed code stream starting at p (2-byte
-// aligned).  Every width is an LSB-first bitstream: 4 bits low nibble first,
-// 2 bits four per byte, 3 bits 8 codes per 3 bytes (the lane's 12 bits start
-// at bit 12*lane, i.e. byte 3*lane/2 plus 0 or 4 bits).
-template <int BITS>
-__device__ __forceinline__ void load_codes(const uint8_t* p, int lane, int (&c)[4])
-{
-    if constexpr (BITS == 2) {
-        const uint32_t w = p[lane];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = (w >> (2 * i)) & 3u;
-    } else if constexpr (BITS == 4) {
-        const uint32_t w = ld_u16(p + 2 * lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = (w >> (4 * i)) & 15u;
-    } else {
-        static_assert(BITS == 3, "2, 3 or 4 bits");
-        const uint8_t* q = p + ((3 * lane) >> 1);
-        const uint32_t w = (uint32_t(q[0]) | uint32_t(q[1]) << 8) >> (4 * (lane & 1));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = (w >> (3 * i)) & 7u;
-    }
-}
-
-template <typename TQ, bool KEY_FP8, int KBITS, int VBITS, int GM>
-__global__ void __launch_bounds__(kWarps * 32) stage1_kernel(DecodeArgs a)
-{
-    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.G, S = a.num_splits;
-    const int L = a.seq_lens[b];
-    const int chunk = (L + S - 1) / S;
-    const int t0 = split * chunk;
-    const int t1 = min(L, t0 + chunk);
-
-    __shared__ float s_cent[16];
-    __shared__ float s_m[kWarps][GM], s_l[kWarps][GM];
-    __shared__ float s_acc[kWarps][GM][kHeadDim];
-
-    if (t0 >= t1) {   // empty split: lse = -inf, zero partial output
-        for (int i = threadIdx.x; i < G * (kHeadDim + 1); i += blockDim.x) {
-            const int g = i / (kHeadDim + 1), d = i % (kHeadDim + 1);
-            float* m = a.mid + (((long long)b * a.Hq + h * G + g) * S + split) * (kHeadDim + 1);
-            m[d] = d == kHeadDim ? -INFINITY : 0.f;
-        }
-        return;
-    }
-    __shared__ int s_bad;        // a block-table entry outside [0, num_blocks) was met
-    if (threadIdx.x == 0) s_bad = 0;
-    if constexpr (!KEY_FP8) {
-        if (threadIdx.x < (1 << KBITS)) s_cent[threadIdx.x] = a.centroids[threadIdx.x];
-    }
-
-    // q (rotated once for MSE keys), pre-multiplied by the softmax scale
-    float qv[GM][4];
-    const TQ* Q = static_cast<const TQ*>(a.query);
-    float sgn[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sgn[i] = KEY_FP8 ? 1.f : float(a.signs[4 * lane + i]);
-#pragma unroll
-    for (int g = 0; g < GM; ++g) {
-        if (g < G) {
-            const TQ* qp = Q + ((long long)b * a.Hq + h * G + g) * kHeadDim + 4 * lane;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qv[g][i] = sgn[i] * to_f32(qp[i]);
-            if constexpr (!KEY_FP8) {
-                fwht128_warp(qv[g], lane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qv[g][i] *= 0.08838834764831845f;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qv[g][i] *= a.scale;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) qv[g][i] = 0.f;
-        }
-    }
-    __syncthreads();
-
-    float m[GM], l[GM], acc[GM][4];
-#pragma unroll
-    for (int g = 0; g < GM; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[g][i] = 0.f;
-    }
-
-    const int32_t* bt = a.block_table + (long long)b * a.bt_stride;
-    const int lgbs = 31 - __clz(a.bs);       // block sizes are powers of two
-    bool bad = false;
-    for (int t = t0 + warp; t < t1; t += kWarps) {
-        const long long page = bt[t >> lgbs];
-        if (page < 0 || page >= a.num_blocks) { bad = true; continue; }   // not read; the rows become NaN
-        const uint8_t *sp, *mp;              // data and metadata of the record
-        slot_ptrs(a.g, a.cache, page, t & (a.bs - 1), h, a.bs, a.Hk, sp, mp);
-
-        float kv[4];
-        float knorm = 1.f;
-        if constexpr (KEY_FP8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                __half_raw hr = __nv_cvt_fp8_to_halfraw(sp[4 * lane + i], __NV_E4M3);
-                kv[i] = __half2float(__half(hr));
-            }
-        } else {
-            int c[4];
-            load_codes<KBITS>(sp, lane, c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kv[i] = s_cent[c[i]];
-            knorm = __half2float(__ushort_as_half(ld_u16(mp + a.g.m_norm)));
-        }
-        float s[GM];
-#pragma unroll
-        for (int g = 0; g < GM; ++g)
-            s[g] = warp_sum(qv[g][0] * kv[0] + qv[g][1] * kv[1] + qv[g][2] * kv[2] + qv[g][3] * kv[3]) * knorm;
-
-        // online softmax; sparse V: a row whose p is at most vthr keeps its
-        // weight in l but adds nothing to the value sum, and the value codes
-        // are not read when no head keeps the row (s is warp-uniform)
-        float al[GM], pv[GM];
-        bool anyv = false;
-#pragma unroll
-        for (int g = 0; g < GM; ++g) {
-            const float mn = fmaxf(m[g], s[g]);
-            const float p = expf(s[g] - mn);
-            al[g] = expf(m[g] - mn);
-            l[g] = l[g] * al[g] + p;
-            m[g] = mn;
-            pv[g] = p > a.vthr ? p : 0.f;
-            anyv |= g < G && pv[g] > 0.f;
-        }
-        float vv[4] = {0.f, 0.f, 0.f, 0.f};
-        if (anyv) {
-            int vc[4];
-            load_codes<VBITS>(sp + a.g.v_off, lane, vc);
-            const float vs = __half2float(__ushort_as_half(ld_u16(mp + a.g.m_scale)));
-            const float vz = __half2float(__ushort_as_half(ld_u16(mp + a.g.m_zero)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vv[i] = float(vc[i]) * vs + vz;
-        }
-#pragma unroll
-        for (int g = 0; g < GM; ++g)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[g][i] = acc[g][i] * al[g] + pv[g] * vv[i];
-    }
-
-    // merge the four warps' partials
-    if (bad && lane == 0) s_bad = 1;
-#pragma unroll
-    for (int g = 0; g < GM; ++g) {
-        if (lane == 0) { s_m[warp][g] = m[g]; s_l[warp][g] = l[g]; }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s_acc[warp][g][4 * lane + i] = acc[g][i];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * kHeadDim; i += blockDim.x) {
-        const int g = i / kHeadDim, d = i % kHeadDim;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][g]);
-        float lsum = 0.f, o = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = s_m[w][g] == -INFINITY ? 0.f : expf(s_m[w][g] - M);
-            lsum += s_l[w][g] * f;
-            o += s_acc[w][g][d] * f;
-        }
-        float* mp = a.mid + (((long long)b * a.Hq + h * G + g) * S + split) * (kHeadDim + 1);
-        mp[d] = o / lsum;
-        if (d == 0) mp[kHeadDim] = s_bad ? __int_as_float(0x7fc00000) : M + logf(lsum);
-    }
-}
 
 // Stage 2: the log-sum-exp merge of the split partials.  A row (sequence,
 // query head) takes R = ceil(S / 16) warps (at most 8), each merging every
@@ -338,41 +140,16 @@ cudaError_t launch_stage2(const DecodeArgs& a, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, stage2_kernel<TO>, a, R);
 }
 
-template <typename TQ, bool FP8, int KB, int VB>
-cudaError_t launch_stage1_g(const DecodeArgs& a, cudaStream_t st)
-{
-    dim3 grid(a.num_splits, a.Hk, a.B);
-    if (a.G <= 1) stage1_kernel<TQ, FP8, KB, VB, 1><<<grid, kWarps * 32, 0, st>>>(a);
-    else if (a.G <= 2) stage1_kernel<TQ, FP8, KB, VB, 2><<<grid, kWarps * 32, 0, st>>>(a);
-    else if (a.G <= 4) stage1_kernel<TQ, FP8, KB, VB, 4><<<grid, kWarps * 32, 0, st>>>(a);
-    else if (a.G <= 8) stage1_kernel<TQ, FP8, KB, VB, 8><<<grid, kWarps * 32, 0, st>>>(a);
-    else stage1_kernel<TQ, FP8, KB, VB, 16><<<grid, kWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
-}
-
-template <typename TQ>
-cudaError_t launch_stage1(int preset, const DecodeArgs& a, cudaStream_t st)
-{
-    switch (preset & 0xFF) {
-    case TQ_K8V4:    return launch_stage1_g<TQ, true, 4, 4>(a, st);
-    case TQ_4BIT_NC: return launch_stage1_g<TQ, false, 4, 4>(a, st);
-    case TQ_K3V4_NC: return launch_stage1_g<TQ, false, 3, 4>(a, st);
-    case TQ_3BIT_NC: return launch_stage1_g<TQ, false, 3, 3>(a, st);
-    case TQ_2BIT_NC: return launch_stage1_g<TQ, false, 2, 2>(a, st);
-    }
-    return cudaErrorInvalidValue;
-}
-
 template <bool FP8, int KB, int VB>
 int v1_slots(int G, int num_sms)
 {
     int per_sm = 0;
     cudaError_t e;
-    if (G <= 1) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 1>, kWarps * 32, 0);
-    else if (G <= 2) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 2>, kWarps * 32, 0);
-    else if (G <= 4) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 4>, kWarps * 32, 0);
-    else if (G <= 8) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 8>, kWarps * 32, 0);
-    else e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 16>, kWarps * 32, 0);
+    if (G <= 1) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 1, false>, kWarps * 32, 0);
+    else if (G <= 2) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 2, false>, kWarps * 32, 0);
+    else if (G <= 4) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 4, false>, kWarps * 32, 0);
+    else if (G <= 8) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 8, false>, kWarps * 32, 0);
+    else e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 16, false>, kWarps * 32, 0);
     return e == cudaSuccess ? per_sm * num_sms : 0;
 }
 
@@ -454,15 +231,28 @@ int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int nu
 namespace tq {
 namespace {
 
+// Host-side checks of score modifiers (device arrays are not read).
+bool mods_ok(const tq_score_mods& m)
+{
+    return m.softcap >= 0.f && m.softcap <= 3.0e38f && m.window >= 0 && m.prefix >= 0;
+}
+
+// Where a call that accumulates attention weights adds them.
+struct WeightsOut {
+    float* acc;
+    long long stride_b, stride_h;
+};
+
 // Argument checks, split choice and the launches of both stages; stuck_tile
-// >= 0 (the wait-expiry test) needs the tensor-core stage 1.
+// >= 0 (the wait-expiry test) needs the tensor-core stage 1.  With `wout` the
+// scores are kept in the workspace and a third kernel adds the weights.
 int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv_heads, int block_size,
                 int q_dtype, const void* query, const uint8_t* kv_cache, long long num_blocks,
                 const int32_t* block_table, int block_table_stride, const int32_t* seq_lens,
                 int max_seq_len, float softmax_scale, int num_splits, const int8_t* signs,
                 const float* centroids, void* out, int out_dtype, float* lse, void* workspace,
                 size_t workspace_bytes, float v_threshold, int stuck_tile, uint32_t wait_polls,
-                void* stream)
+                void* stream, const tq_score_mods* mods = nullptr, const WeightsOut* wout = nullptr)
 {
     tq_layout L;
     int rc = fill_layout(preset, head_dim, &L);
@@ -472,7 +262,7 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
         return TQ_ERR_UNSUPPORTED;
     if (batch < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads ||
         num_blocks < 0 || block_table_stride < 0 || max_seq_len < 0 || num_splits < 0 ||
-        num_splits > TQ_MAX_SPLITS || !(v_threshold >= 0.f && v_threshold < 1.f))
+        num_splits > TQ_MAX_SPLITS || !(v_threshold >= 0.f && v_threshold < 1.f) || (mods && (!mods_ok(*mods) || max_seq_len > kMaxListedLen)))
         return TQ_ERR_INVALID_ARG;
     if (num_q_heads / num_kv_heads > kMaxGroup) return TQ_ERR_UNSUPPORTED;
     if (batch == 0) return TQ_OK;
@@ -481,9 +271,17 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
     if (!L.key_fp8 && (!signs || !centroids)) return TQ_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) & 15) return TQ_ERR_INVALID_ARG;
     const bool soa = is_soa(preset);
-    const int S = num_splits ? num_splits : pick_splits(L, soa, batch, num_q_heads, num_kv_heads, max_seq_len);
-    if (workspace_bytes < tq_decode_workspace_bytes(batch, num_q_heads, S, head_dim))
+    const int G = num_q_heads / num_kv_heads;
+    const int listed = mods ? std::min(max_seq_len, 32 * visible_tiles(max_seq_len, mods->window, mods->prefix))
+                            : max_seq_len;
+    const int S = num_splits ? num_splits : pick_splits(L, soa, batch, num_q_heads, num_kv_heads, listed);
+    if (workspace_bytes < (wout ? tq_decode_weights_workspace_bytes(batch, num_q_heads, num_kv_heads, S, head_dim,
+                                                                    max_seq_len, mods->window, mods->prefix)
+                                : tq_decode_workspace_bytes(batch, num_q_heads, S, head_dim)))
         return TQ_ERR_WORKSPACE;
+    if (wout &&
+        (!wout->acc || !acc_strides_ok(batch, num_kv_heads, wout->stride_b, wout->stride_h, max_seq_len)))
+        return TQ_ERR_INVALID_ARG;
 
     DecodeArgs a;
     a.query = query;
@@ -502,10 +300,31 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
     a.B = batch;
     a.Hq = num_q_heads;
     a.Hk = num_kv_heads;
-    a.G = num_q_heads / num_kv_heads;
+    a.G = G;
     a.bs = block_size;
     a.vthr = v_threshold;
     a.g = geom_of(L, soa);
+    a.mods = ScoreArgs{};
+    if (mods) {
+        a.mods.cap = mods->softcap;
+        a.mods.inv_cap = mods->softcap > 0.f ? 1.f / mods->softcap : 0.f;
+        a.mods.slopes = mods->alibi_slopes;
+        a.mods.window = mods->window;
+        a.mods.prefix = mods->prefix;
+        a.mods.doc_start = mods->doc_start;
+        a.mods.max_len = wout ? max_seq_len : kMaxListedLen;
+    }
+    if (wout) {
+        // after the partials: an lse per query head (used when the caller
+        // wants none), then the scores
+        const WeightsLayout w = weights_layout(batch, num_q_heads, num_kv_heads, S, max_seq_len, mods->window,
+                                               mods->prefix);
+        char* ws = static_cast<char*>(workspace);
+        if (!a.lse) a.lse = reinterpret_cast<float*>(ws + w.off_lse);
+        a.mods.scores = reinterpret_cast<float*>(ws + w.off_scores);
+        a.mods.vtok = w.vtok;
+        a.mods.gp = score_heads(G);
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
 
     const bool mma = mma_stage1_supported(L, soa, num_kv_heads, a.G);
@@ -514,17 +333,24 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
         rc = launch_mma_stage1(L, soa, q_dtype, query, kv_cache, num_blocks, block_table, block_table_stride, seq_lens,
                                softmax_scale, S, signs, centroids, a.mid, batch, num_q_heads,
                                num_kv_heads, block_size, v_threshold, st, stuck_tile,
-                               wait_polls);
+                               wait_polls, mods ? &a.mods : nullptr);
         if (rc) return rc;
+    } else if (mods) {
+        if (launch_cores_scored(preset, q_dtype, a, st) != cudaSuccess) return TQ_ERR_CUDA;
     } else {
-        cudaError_t e = q_dtype == TQ_F16 ? launch_stage1<__half>(preset, a, st)
-                                          : launch_stage1<__nv_bfloat16>(preset, a, st);
+        cudaError_t e = q_dtype == TQ_F16 ? launch_stage1<__half, false>(preset, a, st)
+                                          : launch_stage1<__nv_bfloat16, false>(preset, a, st);
         if (e != cudaSuccess) return TQ_ERR_CUDA;
     }
     const cudaError_t e2 = out_dtype == TQ_F32 ? launch_stage2<float>(a, st)
                            : out_dtype == TQ_F16 ? launch_stage2<__half>(a, st)
                                                  : launch_stage2<__nv_bfloat16>(a, st);
-    return e2 == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+    if (e2 != cudaSuccess) return TQ_ERR_CUDA;
+    if (wout &&
+        launch_weights(a.mods, seq_lens, a.lse, wout->acc, wout->stride_b, wout->stride_h, batch, num_kv_heads, G, st) !=
+            cudaSuccess)
+        return TQ_ERR_CUDA;
+    return TQ_OK;
 }
 
 }  // namespace
@@ -579,6 +405,44 @@ extern "C" int tq_decode_attention(int preset, int head_dim, int batch, int num_
                                         block_table_stride, seq_lens, max_seq_len, softmax_scale,
                                         num_splits, signs, centroids, out, out_dtype, lse, workspace,
                                         workspace_bytes, 0.f, stream);
+}
+
+extern "C" int tq_decode_attention_scored(int preset, int head_dim, int batch, int num_q_heads,
+                                          int num_kv_heads, int block_size, int q_dtype,
+                                          const void* query, const uint8_t* kv_cache,
+                                          long long num_blocks, const int32_t* block_table,
+                                          int block_table_stride, const int32_t* seq_lens,
+                                          int max_seq_len, float softmax_scale, int num_splits,
+                                          const int8_t* signs, const float* centroids, void* out,
+                                          int out_dtype, float* lse, void* workspace,
+                                          size_t workspace_bytes, const tq_score_mods* mods, void* stream)
+{
+    // no modifier: the plain decode
+    const bool plain = !mods || (mods->softcap == 0.f && mods->window == 0 && !mods->alibi_slopes &&
+                                 !mods->doc_start && mods->prefix >= 0);
+    return tq::decode_impl(preset, head_dim, batch, num_q_heads, num_kv_heads, block_size, q_dtype, query,
+                           kv_cache, num_blocks, block_table, block_table_stride, seq_lens, max_seq_len,
+                           softmax_scale, num_splits, signs, centroids, out, out_dtype, lse, workspace,
+                           workspace_bytes, 0.f, -1, tq::kWaitPolls, stream, plain ? nullptr : mods);
+}
+
+extern "C" int tq_decode_attention_weights(int preset, int head_dim, int batch, int num_q_heads,
+                                           int num_kv_heads, int block_size, int q_dtype,
+                                           const void* query, const uint8_t* kv_cache,
+                                           long long num_blocks, const int32_t* block_table,
+                                           int block_table_stride, const int32_t* seq_lens,
+                                           int max_seq_len, float softmax_scale, int num_splits,
+                                           const int8_t* signs, const float* centroids, void* out,
+                                           int out_dtype, float* lse, void* workspace,
+                                           size_t workspace_bytes, const tq_score_mods* mods, float* acc,
+                                           long long acc_stride_seq, long long acc_stride_head, void* stream)
+{
+    const tq_score_mods none = {};
+    const tq::WeightsOut w = {acc, acc_stride_seq, acc_stride_head};
+    return tq::decode_impl(preset, head_dim, batch, num_q_heads, num_kv_heads, block_size, q_dtype, query,
+                           kv_cache, num_blocks, block_table, block_table_stride, seq_lens, max_seq_len,
+                           softmax_scale, num_splits, signs, centroids, out, out_dtype, lse, workspace,
+                           workspace_bytes, 0.f, -1, tq::kWaitPolls, stream, mods ? mods : &none, &w);
 }
 
 extern "C" int tq_decode_kernel_kind(int preset, int head_dim, int num_q_heads, int num_kv_heads)

@@ -12,8 +12,8 @@ namespace tq {
 
 cudaError_t launch_mma_dense(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st)
 {
-    return q_dtype == TQ_F16 ? launch_q<__half, false>(a, B, smem, st)
-                             : launch_q<__nv_bfloat16, false>(a, B, smem, st);
+    return q_dtype == TQ_F16 ? launch_q<__half, kDense>(a, B, smem, st)
+                             : launch_q<__nv_bfloat16, kDense>(a, B, smem, st);
 }
 
 namespace {
@@ -155,8 +155,8 @@ MmaGeom mma_geom(const tq_layout& L, bool soa, int Hk, int G)
 template <int KMODE, int VBITS, int G>
 int slots_t(const MmaGeom& m, bool soa, int num_sms)
 {
-    auto k = soa ? stage1_mma_kernel<__nv_bfloat16, KMODE, VBITS, G, true, false>
-                 : stage1_mma_kernel<__nv_bfloat16, KMODE, VBITS, G, false, false>;
+    auto k = soa ? stage1_mma_kernel<__nv_bfloat16, KMODE, VBITS, G, true, kDense>
+                 : stage1_mma_kernel<__nv_bfloat16, KMODE, VBITS, G, false, kDense>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(m.smem)) != cudaSuccess)
         return 0;
     int per_sm = 0;
@@ -232,7 +232,7 @@ int launch_mma_stage1(const tq_layout& L, bool soa, int q_dtype, const void* que
                       float softmax_scale, int num_splits, const int8_t* signs,
                       const float* centroids, float* mid, int B, int Hq, int Hk, int bs,
                       float v_threshold, cudaStream_t st, int stuck_tile,
-                      uint32_t wait_polls)
+                      uint32_t wait_polls, const ScoreArgs* mods)
 {
     MmaArgs a;
     a.vthr = v_threshold;
@@ -279,8 +279,10 @@ int launch_mma_stage1(const tq_layout& L, bool soa, int q_dtype, const void* que
     a.nstages = m.nstages;
     a.g = geom_of(L, soa);
     a.lpt = (B <= 512 && m.smem >= size_t(4) * (B + 1)) ? 1 : 0;
-    const cudaError_t e = v_threshold > 0.f ? launch_mma_sparse(a, q_dtype, B, m.smem, st)
-                                            : launch_mma_dense(a, q_dtype, B, m.smem, st);
+    a.mods = mods ? *mods : ScoreArgs{};
+    const cudaError_t e = mods                ? launch_mma_scored(a, q_dtype, B, m.smem, st)
+                          : v_threshold > 0.f ? launch_mma_sparse(a, q_dtype, B, m.smem, st)
+                                              : launch_mma_dense(a, q_dtype, B, m.smem, st);
     return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

@@ -80,12 +80,18 @@ struct MmaArgs {
     int stuck_tile;          // test hook: this tile of split 0, sequence 0, head group 0 is
                              // expected 16 bytes more than its copies bring (-1: none)
     SlotGeom g;
+    ScoreArgs mods;          // kScored instantiations only
 };
 
-// Stage 1 with the value sum of every row (dense) or with the sparse-V gate;
-// each is instantiated in its own translation unit.
+// What a stage-1 instantiation does beyond the plain decode: the sparse-V
+// gate, or the score modifiers (softcap, distance bias, visible tokens) with
+// the scores kept for the attention weights when asked.
+constexpr int kDense = 0, kSparse = 1, kScored = 2;
+
+// Each mode is instantiated in its own translation unit.
 cudaError_t launch_mma_dense(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
 cudaError_t launch_mma_sparse(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
+cudaError_t launch_mma_scored(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
 
 namespace {
 
@@ -629,9 +635,11 @@ __device__ __forceinline__ void pv_tile(const uint8_t* tile_v, int rs, int gid, 
 // G: 4 (columns = 4 heads x {hi, lo}) or 8 (columns = 8 heads).
 // One CTA = (split, sequence); warp w = kv head w; each iteration consumes a
 // 32-token tile (two 16-row MMA tiles) with one softmax update.
-template <typename TQ, int KMODE, int VBITS, int G, bool SOA, bool SPARSE>
+// MODE: kDense, kSparse or kScored.
+template <typename TQ, int KMODE, int VBITS, int G, bool SOA, int MODE>
 __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__ MmaArgs a)
 {
+    constexpr bool SPARSE = MODE == kSparse, SCORED = MODE == kScored;
     extern __shared__ __align__(128) uint8_t smem[];
     // 3-bit keys: the code-pair centroid table (8 KB; one element elsewhere)
     __shared__ __align__(16) uint2 key_lut[KMODE == 3 ? kLut3Entries : KMODE == 4 ? kLut4Entries : 1];
@@ -664,10 +672,20 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int L = a.seq_lens[b];
     int chunk = (L + S - 1) / S;
     chunk = (chunk + kTile - 1) / kTile * kTile;
-    const int t_begin = split * chunk;
-    const int t_end = min(L, t_begin + chunk);
+    int t_begin = split * chunk;
+    int t_end = min(L, t_begin + chunk);
+    // scored: the splits share the tiles that hold visible tokens; t_begin and
+    // t_end are then positions in that list (32 per tile)
+    bool too_long = false;       // past what can be listed: a NaN lse, nothing read
+    [[maybe_unused]] VisibleSet vis(SCORED ? a.mods : ScoreArgs{}, SCORED ? min(L, a.mods.max_len) : 0, b);
+    if constexpr (SCORED) {
+        chunk = (vis.tiles() + S - 1) / S * kTile;
+        t_begin = split * chunk;
+        t_end = min(vis.tiles() * kTile, t_begin + chunk);
+        too_long = L > a.mods.max_len;
+    }
 
-    if (t_begin >= t_end || a.num_blocks <= 0) {
+    if (t_begin >= t_end || a.num_blocks <= 0 || (SCORED && too_long)) {
         // empty split: lse = -inf and a zero partial; tokens but no cache
         // block to read them from: a NaN lse
         const float lse0 = t_begin >= t_end ? -INFINITY : __int_as_float(0x7fc00000);
@@ -745,7 +763,7 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         if (tile >= ntiles) return;
         uint8_t* dst = smem + stage * stage_bytes;
         uint64_t* bar = &full[stage];
-        const int tbase = t_begin + tile * kTile;
+        const int tbase = SCORED ? vis.base((t_begin >> 5) + tile) : t_begin + tile * kTile;
         // data rows: one copy per page segment when the CTA takes whole rows
         // and the shared stride equals the global one, or through the tensor
         // map (a box of the CTA's part of a segment's rows), else one per
@@ -757,20 +775,30 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         const int lg_d = seg_d ? seg_lg : 0, lg_m = seg_m ? seg_lg : 0;      // (powers of two)
         const int nd = min(kTile >> lg_d, (L - tbase + len_d - 1) >> lg_d);
         const int nm = soa ? min(kTile >> lg_m, (L - tbase + len_m - 1) >> lg_m) : 0;
+        // scored: only copies that bring a visible token (the pages of others
+        // may have been freed)
+        bool want_d = lane < nd, want_m = lane < nm;
+        int cnt_d = nd, cnt_m = nm;
+        if constexpr (SCORED) {
+            want_d = want_d && vis.any(tbase + lane * len_d, len_d);
+            want_m = want_m && vis.any(tbase + lane * len_m, len_m);
+            cnt_d = __popc(__ballot_sync(0xffffffffu, want_d));
+            if constexpr (soa) cnt_m = __popc(__ballot_sync(0xffffffffu, want_m));
+        }
         if (lane == 0) {
             fence_async_shared();             // prior generic reads of this stage before the async writes
             // the test hook's tile expects 16 bytes that no copy brings: its
             // stage never completes and the bounded waits run out
             const uint32_t extra =
                 (tile == a.stuck_tile && split == 0 && qg == 0 && b == 0 && kvg == 0) ? 16u : 0u;
-            mbar_expect_tx(bar, uint32_t(nd * len_d * cb + nm * len_m * mb) + extra);
+            mbar_expect_tx(bar, uint32_t(cnt_d * len_d * cb + cnt_m * len_m * mb) + extra);
         }
         __syncwarp();
         const bool same = !soa || len_d == len_m;     // one address computation for both copies
         // a block-table entry outside [0, num_blocks) is replaced by page 0,
         // so nothing outside the cache is read, and noted: the CTA's rows
         // come out NaN (see the end of the kernel)
-        if (lane < nd) {
+        if (want_d) {
             const int t = tbase + lane * len_d;
             long long page = bt[t >> lg];
             if ((unsigned long long)page >= (unsigned long long)a.num_blocks) { page = 0; bad_seen = true; }
@@ -788,7 +816,7 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
                 bulk_g2s(dst + kTile * rs + lane * len_m * mb, meta, uint32_t(len_m * mb), bar);
             }
         }
-        if (!same && lane < nm) {
+        if (!same && want_m) {
             const int t = tbase + lane * len_m;
             long long page = bt[t >> lg];
             if ((unsigned long long)page >= (unsigned long long)a.num_blocks) { page = 0; bad_seen = true; }
@@ -957,13 +985,31 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int mrs = soa ? mb : rs;
     const int moff = soa ? kTile * rs + warp * a.g.meta_bytes : hoff;
 
+    // scored: the cap and the head's slopes in log2 units, and this thread's
+    // score column (query heads qh0 + tig, or qh0 + 2 tig and the next)
+    [[maybe_unused]] float cap2 = 0.f, inv_cap2 = 0.f, slope2[NH] = {};
+    [[maybe_unused]] float* sc_out = nullptr;
+    if constexpr (SCORED) {
+        constexpr float kLog2e = 1.4426950408889634f;
+        cap2 = a.mods.cap * kLog2e;
+        inv_cap2 = a.mods.inv_cap * (1.f / kLog2e);
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+            const int g = G == 4 ? tig : 2 * tig + j;
+            if (a.mods.slopes && g < Greal) slope2[j] = a.mods.slopes[h * Gall + qh0 + g] * kLog2e;
+        }
+        if (a.mods.scores)
+            sc_out = a.mods.scores + ((long long)b * a.Hk + h) * a.mods.vtok * a.mods.gp + qh0 + (G == 4 ? tig : 2 * tig);
+    }
+
     // One 32-token tile in stage memory st (this warp's slot at offset 0).
     // PARTIAL: some of its tokens lie at or past t_end and are masked.
     // KGEN: the general key path; false: 2-bit keys without the lo part
     // (key_alpha)
     // KM / VM: the key / value misalignment of this warp's slot (0 or 2)
-    auto tile = [&](const uint8_t* st, const uint8_t* sm, int t0, auto partial_tag, auto lo_tag,
-                    auto km_tag, auto vm_tag) {
+    // vt: scored, the tile's first position in the list of visible tiles
+    auto tile = [&](const uint8_t* st, const uint8_t* sm, int t0, [[maybe_unused]] int vt, auto partial_tag,
+                    auto lo_tag, auto km_tag, auto vm_tag) {
         constexpr bool PARTIAL = decltype(partial_tag)::value;
         [[maybe_unused]] constexpr bool KGEN = decltype(lo_tag)::value;
         constexpr int KM = decltype(km_tag)::value, VM = decltype(vm_tag)::value;
@@ -995,8 +1041,13 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             vz[rt][0] = lds_f16(m0 + a.g.m_zero);
             vs[rt][1] = lds_f16(m1 + a.g.m_scale);
             vz[rt][1] = lds_f16(m1 + a.g.m_zero);
-            ok[rt][0] = !PARTIAL || t0 + 16 * rt + tau0 < t_end;
-            ok[rt][1] = !PARTIAL || t0 + 16 * rt + tau1 < t_end;
+            if constexpr (SCORED) {
+                ok[rt][0] = !PARTIAL || vis.sees(t0 + 16 * rt + tau0);
+                ok[rt][1] = !PARTIAL || vis.sees(t0 + 16 * rt + tau1);
+            } else {
+                ok[rt][0] = !PARTIAL || t0 + 16 * rt + tau0 < t_end;
+                ok[rt][1] = !PARTIAL || t0 + 16 * rt + tau1 < t_end;
+            }
             if constexpr (G == 4) {
                 s[0][rt][0] = (sc[0] + sc[1]) * n0;
                 s[0][rt][1] = (sc[2] + sc[3]) * n1;
@@ -1005,6 +1056,28 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
                 s[1][rt][0] = (sc[1] + scl[1]) * n0;
                 s[0][rt][1] = (sc[2] + scl[2]) * n1;
                 s[1][rt][1] = (sc[3] + scl[3]) * n1;
+            }
+        }
+
+        if constexpr (SCORED) {
+            // softcap, then the distance bias (distance: to the newest token)
+            if (a.mods.cap > 0.f) {
+#pragma unroll
+                for (int j = 0; j < NH; ++j)
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) s[j][rt][r] = cap2 * tanhf(s[j][rt][r] * inv_cap2);
+            }
+            if (a.mods.slopes) {
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float dist = float(L - 1 - (t0 + 16 * rt + (r ? tau1 : tau0)));
+#pragma unroll
+                        for (int j = 0; j < NH; ++j) s[j][rt][r] = fmaf(-slope2[j], dist, s[j][rt][r]);
+                    }
             }
         }
 
@@ -1029,8 +1102,24 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            mt[j] = m;               // finite: the tile's first token is valid
+            mt[j] = m;               // finite: the tile holds a valid token
             need |= m > m_run[j] + 8.f;
+        }
+        if constexpr (SCORED) {
+            // the scores for the attention weights, masked tokens as -inf
+            if (a.mods.scores) {
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float* sp = sc_out + (long long)(vt + 16 * rt + (r ? tau1 : tau0)) * a.mods.gp;
+                        if constexpr (G == 4) {
+                            if (tig < Greal) *sp = s[0][rt][r];
+                        } else {
+                            if (2 * tig < Greal) *reinterpret_cast<float2*>(sp) = make_float2(s[0][rt][r], s[1][rt][r]);
+                        }
+                    }
+            }
         }
         need |= fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1])) > 128.f;
         if (__any_sync(0xffffffffu, need)) {
@@ -1103,9 +1192,11 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             if (!__all_sync(0xffffffffu, ok_wait)) return it;
             const uint8_t* st = smem + stage * stage_bytes + hoff;
             const uint8_t* sm = smem + stage * stage_bytes + moff;
-            const int t0 = t_begin + it * kTile;
-            if (t0 + kTile <= t_end) tile(st, sm, t0, std::false_type{}, lo_tag, km_tag, vm_tag);
-            else                     tile(st, sm, t0, std::true_type{}, lo_tag, km_tag, vm_tag);
+            const int vt = t_begin + it * kTile;
+            const int t0 = SCORED ? vis.base(vt >> 5) : vt;
+            const bool whole = SCORED ? vis.all(t0, kTile) : vt + kTile <= t_end;
+            if (whole) tile(st, sm, t0, vt, std::false_type{}, lo_tag, km_tag, vm_tag);
+            else       tile(st, sm, t0, vt, std::true_type{}, lo_tag, km_tag, vm_tag);
 
             // ---- this warp is done with the stage; the last warp refills it
             __syncwarp();
@@ -1218,11 +1309,11 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     }
 }
 
-template <typename TQ, int KMODE, int VBITS, int G, bool SPARSE>
+template <typename TQ, int KMODE, int VBITS, int G, int MODE>
 cudaError_t launch_t(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
 {
-    auto k = a.g.soa ? stage1_mma_kernel<TQ, KMODE, VBITS, G, true, SPARSE>
-                     : stage1_mma_kernel<TQ, KMODE, VBITS, G, false, SPARSE>;
+    auto k = a.g.soa ? stage1_mma_kernel<TQ, KMODE, VBITS, G, true, MODE>
+                     : stage1_mma_kernel<TQ, KMODE, VBITS, G, false, MODE>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1238,21 +1329,21 @@ cudaError_t launch_t(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-template <typename TQ, int KMODE, int VBITS, bool SPARSE>
+template <typename TQ, int KMODE, int VBITS, int MODE>
 cudaError_t launch_g(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
 {
-    return a.G <= 4 ? launch_t<TQ, KMODE, VBITS, 4, SPARSE>(a, B, smem, st)
-                    : launch_t<TQ, KMODE, VBITS, 8, SPARSE>(a, B, smem, st);
+    return a.G <= 4 ? launch_t<TQ, KMODE, VBITS, 4, MODE>(a, B, smem, st)
+                    : launch_t<TQ, KMODE, VBITS, 8, MODE>(a, B, smem, st);
 }
 
-template <typename TQ, bool SPARSE>
+template <typename TQ, int MODE>
 cudaError_t launch_q(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
 {
-    if (a.g.key_fp8) return launch_g<TQ, 8, 4, SPARSE>(a, B, smem, st);
-    if (a.g.key_bits == 4) return launch_g<TQ, 4, 4, SPARSE>(a, B, smem, st);
-    if (a.g.key_bits == 2) return launch_g<TQ, 2, 2, SPARSE>(a, B, smem, st);
-    if (a.g.value_bits == 4) return launch_g<TQ, 3, 4, SPARSE>(a, B, smem, st);
-    return launch_g<TQ, 3, 3, SPARSE>(a, B, smem, st);
+    if (a.g.key_fp8) return launch_g<TQ, 8, 4, MODE>(a, B, smem, st);
+    if (a.g.key_bits == 4) return launch_g<TQ, 4, 4, MODE>(a, B, smem, st);
+    if (a.g.key_bits == 2) return launch_g<TQ, 2, 2, MODE>(a, B, smem, st);
+    if (a.g.value_bits == 4) return launch_g<TQ, 3, 4, MODE>(a, B, smem, st);
+    return launch_g<TQ, 3, 3, MODE>(a, B, smem, st);
 }
 
 }  // namespace

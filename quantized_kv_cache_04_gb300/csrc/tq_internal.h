@@ -90,6 +90,112 @@ __device__ __forceinline__ void slot_ptrs(const SlotGeom& g, const uint8_t* cach
 }
 #endif
 
+// Longest sequence the scored decode and the eviction take: positions of
+// 32-token tiles then stay clear of 2^31.
+constexpr int kMaxListedLen = 1 << 30;
+
+// Score modifiers as the stage-1 kernels take them (tq_score_mods in tq.h),
+// and where the scores of a call that accumulates attention weights go.
+struct ScoreArgs {
+    float cap, inv_cap;        // softcap and its reciprocal (cap 0: none)
+    const float* slopes;       // distance biases per query head (null: none)
+    int window, prefix;        // window 0: every token of the document
+    const int32_t* doc_start;  // first token of the current document (null: 0)
+    float* scores;             // [B][Hk][vtok][gp] scores in log2 units (null: not kept)
+    int vtok;                  // listed tokens per (sequence, kv head): a multiple of 32
+    int gp;                    // query heads per kv head, padded (score_heads)
+    int max_len;               // sequences longer than this cannot be listed: a NaN lse
+};
+
+// columns per listed token in ScoreArgs::scores: even above 4 heads, where
+// the tensor-core stage 1 writes pairs
+inline int score_heads(int G) { return G <= 4 ? G : (G + 1) & ~1; }
+
+// 32-token tiles that hold the visible tokens of a sequence of at most
+// max_len tokens (VisibleSet): a window or prefix of n tokens meets at most
+// n / 32 + 2 of them
+inline int visible_tiles(int max_len, int window, int prefix)
+{
+    const long long all = ((long long)max_len + 31) / 32;
+    if (window <= 0) return int(all);
+    const long long some = (long long)window / 32 + 2 + (prefix > 0 ? (long long)prefix / 32 + 2 : 0);
+    return int(all < some ? all : some);
+}
+
+// The workspace of a call that accumulates attention weights: the split
+// partials, an lse per query head, the scores; byte offsets on 256-byte
+// boundaries.
+struct WeightsLayout {
+    size_t off_lse, off_scores, bytes;
+    int vtok;
+};
+inline WeightsLayout weights_layout(int batch, int Hq, int Hk, int S, int max_len, int window, int prefix)
+{
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    WeightsLayout w;
+    w.vtok = 32 * visible_tiles(max_len, window, prefix);
+    w.off_lse = up(tq_decode_workspace_bytes(batch, Hq, S, kHeadDim));
+    w.off_scores = w.off_lse + up(size_t(batch) * Hq * sizeof(float));
+    w.bytes = w.off_scores + size_t(batch) * Hk * w.vtok * score_heads(Hq / Hk) * sizeof(float);
+    return w;
+}
+
+// Whether rows acc + b * sb + h * sh of max_len elements do not overlap:
+// sequences of heads or heads of sequences (one writer per running sum).
+inline bool acc_strides_ok(int B, int Hk, long long sb, long long sh, int max_len)
+{
+    if (sb < 0 || sh < 0) return false;
+    if (Hk > 1 && sh < max_len) return false;
+    if (B > 1 && sb < max_len) return false;
+    if (B <= 1 || Hk <= 1) return true;
+    return sb >= (Hk - 1) * sh + max_len || sh >= (B - 1) * sb + max_len;
+}
+
+// acc[b][h][t] += sum of the softmax weights of token t over the G query
+// heads of kv head h, from the kept scores and the lse (tq_weights.cu).
+cudaError_t launch_weights(const ScoreArgs& m, const int32_t* seq_lens, const float* lse, float* acc,
+                           long long stride_b, long long stride_h, int B, int Hk, int G, cudaStream_t st);
+
+#ifdef __CUDACC__
+// The visible tokens of a sequence: [lo, pend) and [first, L), with
+// lo <= pend <= first, listed by the 32-token tiles (of the sequence) that
+// hold any of them: tiles a0 .. a0 + na - 1 for the prefix, then b0 ..
+// b0 + nb - 1.  Every listed tile holds a visible token; tiles between the
+// prefix and the window are not listed, so their pages are never looked at.
+struct VisibleSet {
+    int L, lo, pend, first;
+    int a0, na, b0, nb;
+    __device__ __forceinline__ VisibleSet(const ScoreArgs& m, int len, int b)
+    {
+        L = max(len, 0);
+        lo = m.doc_start ? max(m.doc_start[b], 0) : 0;
+        lo = min(lo, L);
+        first = m.window > 0 ? max(lo, L - m.window) : lo;
+        pend = lo + (m.window > 0 ? min(m.prefix, first - lo) : 0);
+        a0 = lo >> 5;
+        na = pend > lo ? ((pend + 31) >> 5) - a0 : 0;
+        b0 = max(first >> 5, na ? a0 + na : 0);
+        nb = first < L ? max(((L + 31) >> 5) - b0, 0) : 0;
+    }
+    __device__ __forceinline__ int tiles() const { return na + nb; }
+    // first token of listed tile v
+    __device__ __forceinline__ int base(int v) const { return (v < na ? a0 + v : b0 + v - na) << 5; }
+    __device__ __forceinline__ bool sees(int t) const
+    {
+        return (t >= lo && t < pend) || (t >= first && t < L);
+    }
+    // whether [t, t + n) holds a visible token / nothing else
+    __device__ __forceinline__ bool any(int t, int n) const
+    {
+        return max(t, lo) < min(t + n, pend) || max(t, first) < min(t + n, L);
+    }
+    __device__ __forceinline__ bool all(int t, int n) const
+    {
+        return (t >= lo && t + n <= pend) || (t >= first && t + n <= L);
+    }
+};
+#endif
+
 // Tensor-core stage 1 (tq_decode_mma.cu): which shapes it serves, and its launcher.
 bool mma_stage1_supported(const tq_layout& L, bool soa, int num_kv_heads, int group);
 // CTAs one split of one sequence launches, and resident CTA slots on num_sms
@@ -106,6 +212,6 @@ int launch_mma_stage1(const tq_layout& L, bool soa, int q_dtype, const void* que
                       float softmax_scale, int num_splits, const int8_t* signs,
                       const float* centroids, float* mid, int B, int Hq, int Hk, int bs,
                       float v_threshold, cudaStream_t st, int stuck_tile = -1,
-                      uint32_t wait_polls = kWaitPolls);
+                      uint32_t wait_polls = kWaitPolls, const ScoreArgs* mods = nullptr);
 
 }  // namespace tq
