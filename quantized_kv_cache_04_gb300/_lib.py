@@ -9,6 +9,7 @@ loaded, every call raises: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import build as _build
@@ -277,27 +278,28 @@ def decode_attention(preset: int, query, kv_cache, block_table, seq_lens, max_se
         raise TQError("tq_decode_attention", rc)
 
 
+# Checks of the scored decode and the eviction.  Each helper tests everything in
+# one expression first and words a refusal only when that fails: the calls are
+# a few microseconds of GPU work on short contexts.
 def _need(ok: bool, fn: str, what: str) -> None:
     if not ok:
         raise ValueError(f"{fn}: {what}")
 
 
-def _on(t, device, dtypes, shape, fn: str, name: str, contiguous: bool = True) -> None:
-    """t is a tensor of one of `dtypes` on `device` with this shape (None: any size)."""
+def _on(t, dev: int, dtypes, shape, fn: str, name: str, contiguous: bool = True) -> None:
+    """t is a tensor of one of `dtypes` on GPU `dev` with this shape (None: any size)."""
     import torch
     _need(isinstance(t, torch.Tensor), fn, f"{name} is not a tensor")
-    _need(t.device == device and t.is_cuda, fn, f"{name} is on {t.device}, not on the call's GPU {device}")
+    _need(t.is_cuda and t.get_device() == dev, fn, f"{name} is on {t.device}, not on the GPU of the call's first tensor")
     _need(t.dtype in dtypes, fn, f"{name} has dtype {t.dtype}")
     _need(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)), fn,
           f"{name} has shape {tuple(t.shape)}, expected {shape}")
     _need(not contiguous or t.is_contiguous(), fn, f"{name} is not contiguous")
 
 
-def _table_and_lens(fn, device, block_table, seq_lens, B: int):
-    import torch
-    _on(block_table, device, (torch.int32,), (B, None), fn, "block_table", contiguous=False)
-    _need(block_table.shape[1] <= 1 or block_table.stride(1) == 1, fn, "block_table rows are not contiguous")
-    _on(seq_lens, device, (torch.int32,), (B,), fn, "seq_lens")
+def _rows_ok(t) -> bool:
+    """Contiguous innermost rows (any strides above them)."""
+    return t.shape[-1] <= 1 or t.stride(-1) == 1
 
 
 def _acc_strides(acc):
@@ -307,21 +309,24 @@ def _acc_strides(acc):
     return (acc.stride(0) if B > 1 else Hk * sh), sh
 
 
-class _Device:
-    """The tensors' GPU as the current one, and the stream of a call on it."""
+@functools.lru_cache(maxsize=None)
+def _slot_of(preset: int, head_dim: int):
+    """(slot bytes, FP8 keys, centroids) of a preset."""
+    lay = tq_get_layout(preset, head_dim)
+    return lay["slot_size_aligned"], bool(lay["key_fp8"]), lay["n_centroids"]
 
-    def __init__(self, device, stream):
-        import torch
-        self.guard, self.device, self.stream = torch.cuda.device(device), device, stream
 
-    def __enter__(self):
-        import torch
-        self.guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+def _enqueue(name: str, dev: int, stream, args) -> None:
+    """One C call with `dev` as the current GPU, on `stream` (None: its current stream)."""
+    import torch
+    f = getattr(load(), name)
+    if dev == torch.cuda.current_device():
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise TQError(name, rc)
 
 
 def _listed_len(max_seq_len: int, window: int, prefix: int) -> int:
@@ -347,35 +352,80 @@ def scored_workspace_bytes(preset: int, batch: int, num_q_heads: int, num_kv_hea
     return max(16, n)
 
 
-def _scored_args(fn, preset, query, kv_cache, block_table, seq_lens, max_seq_len, num_kv_heads, block_size, signs,
-                 centroids, out, lse, workspace, num_splits, softmax_scale, softcap, alibi_slopes, window,
-                 prefix, doc_start):
+def _scored_refusal(fn, dev, dt, query, kv_cache, block_table, seq_lens, num_kv_heads, block_size, signs, centroids,
+                    out, lse, workspace, alibi_slopes, doc_start, slot, fp8, n_cent):
+    """Words what _scored_args found wrong."""
     import torch
-    dev = query.device
-    _on(query, dev, (torch.float16, torch.bfloat16), (None, None, None), fn, "query")
     B, Hq, D = query.shape
-    _on(out, dev, (torch.float16, torch.bfloat16, torch.float32), (B, Hq, D), fn, "out")
+    _on(query, dev, dt["half"], (None, None, None), fn, "query")
+    _on(out, dev, dt["any"], (B, Hq, D), fn, "out")
     if lse is not None:
         _on(lse, dev, (torch.float32,), (B, Hq), fn, "lse")
-    _table_and_lens(fn, dev, block_table, seq_lens, B)
-    lay = tq_get_layout(int(preset), D)
-    _on(kv_cache, dev, (torch.uint8,), (None, int(block_size), int(num_kv_heads), lay["slot_size_aligned"]), fn,
-        "kv_cache")
-    if not lay["key_fp8"]:
+    _on(block_table, dev, (torch.int32,), (B, None), fn, "block_table", contiguous=False)
+    _need(_rows_ok(block_table), fn, "block_table rows are not contiguous")
+    _on(seq_lens, dev, (torch.int32,), (B,), fn, "seq_lens")
+    _on(kv_cache, dev, (torch.uint8,), (None, block_size, num_kv_heads, slot), fn, "kv_cache")
+    if not fp8:
         _on(signs, dev, (torch.int8,), (D,), fn, "signs")
-        _on(centroids, dev, (torch.float32,), (lay["n_centroids"],), fn, "centroids")
-    _need(workspace.device == dev and workspace.is_contiguous(), fn, "workspace is not contiguous memory of the call's GPU")
+        _on(centroids, dev, (torch.float32,), (n_cent,), fn, "centroids")
+    _need(isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous(), fn,
+          "workspace is not contiguous memory of the call's GPU")
     if alibi_slopes is not None:
         _on(alibi_slopes, dev, (torch.float32,), (Hq,), fn, "alibi_slopes")
     if doc_start is not None:
         _on(doc_start, dev, (torch.int32,), (B,), fn, "doc_start")
-    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
-    mods = TQScoreMods(float(softcap), int(window), int(prefix), _ptr(alibi_slopes) or None, _ptr(doc_start) or None)
-    return (int(preset), D, B, Hq, int(num_kv_heads), int(block_size), _dtype_code(query), _ptr(query),
-            _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table), block_table.stride(0), _ptr(seq_lens),
-            int(max_seq_len), scale, int(num_splits), _ptr(signs), _ptr(centroids), _ptr(out),
-            _dtype_code(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            ctypes.byref(mods))
+    raise ValueError(f"{fn}: arguments do not fit together")
+
+
+@functools.lru_cache(maxsize=None)
+def _dtypes():
+    import torch
+    return {"half": {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16},
+            "any": {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16, torch.float32: TQ_F32},
+            "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8, "i8": torch.int8, "tensor": torch.Tensor}
+
+
+def _scored_args(fn, preset, query, kv_cache, block_table, seq_lens, max_seq_len, num_kv_heads, block_size, signs,
+                 centroids, out, lse, workspace, num_splits, softmax_scale, softcap, alibi_slopes, window,
+                 prefix, doc_start):
+    dt = _dtypes()
+    _need(isinstance(query, dt["tensor"]) and query.is_cuda and query.dim() == 3, fn,
+          "query is not a (B, Hq, D) tensor of a GPU")
+    f32, i32 = dt["f32"], dt["i32"]
+    dev = query.get_device()
+    preset, num_kv_heads, block_size, max_seq_len = int(preset), int(num_kv_heads), int(block_size), int(max_seq_len)
+    B, Hq, D = shape = query.shape
+    slot, fp8, n_cent = _slot_of(preset, D)
+    cshape = kv_cache.shape
+    if not (query.dtype in dt["half"] and query.is_contiguous()
+            and out.get_device() == dev and out.dtype in dt["any"] and out.shape == shape and out.is_contiguous()
+            and (lse is None or (lse.get_device() == dev and lse.dtype is f32 and lse.shape == shape[:2]
+                                 and lse.is_contiguous()))
+            and block_table.get_device() == dev and block_table.dtype is i32 and block_table.dim() == 2
+            and block_table.shape[0] == B and _rows_ok(block_table)
+            and seq_lens.get_device() == dev and seq_lens.dtype is i32 and seq_lens.shape == (B,)
+            and seq_lens.is_contiguous()
+            and kv_cache.get_device() == dev and kv_cache.dtype is dt["u8"]
+            and cshape[1:] == (block_size, num_kv_heads, slot) and kv_cache.is_contiguous()
+            and (fp8 or (signs is not None and signs.get_device() == dev and signs.dtype is dt["i8"]
+                         and signs.shape == (D,) and signs.is_contiguous()
+                         and centroids is not None and centroids.get_device() == dev and centroids.dtype is f32
+                         and centroids.shape == (n_cent,) and centroids.is_contiguous()))
+            and workspace.get_device() == dev and workspace.is_contiguous()
+            and (alibi_slopes is None or (alibi_slopes.get_device() == dev and alibi_slopes.dtype is f32
+                                          and alibi_slopes.shape == (Hq,) and alibi_slopes.is_contiguous()))
+            and (doc_start is None or (doc_start.get_device() == dev and doc_start.dtype is i32
+                                       and doc_start.shape == (B,) and doc_start.is_contiguous()))):
+        _scored_refusal(fn, dev, dt, query, kv_cache, block_table, seq_lens, num_kv_heads, block_size, signs,
+                        centroids, out, lse, workspace, alibi_slopes, doc_start, slot, fp8, n_cent)
+    mods = TQScoreMods(float(softcap), int(window), int(prefix), None if alibi_slopes is None else alibi_slopes.data_ptr(),
+                       None if doc_start is None else doc_start.data_ptr())
+    return dev, (preset, D, B, Hq, num_kv_heads, block_size, dt["half"][query.dtype], query.data_ptr(),
+                 kv_cache.data_ptr(), cshape[0], block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(),
+                 max_seq_len, D ** -0.5 if softmax_scale is None else float(softmax_scale), int(num_splits),
+                 None if signs is None else signs.data_ptr(), None if centroids is None else centroids.data_ptr(),
+                 out.data_ptr(), dt["any"][out.dtype], None if lse is None else lse.data_ptr(),
+                 workspace.data_ptr(), workspace.nbytes, ctypes.byref(mods))
 
 
 def decode_attention_scored(preset: int, query, kv_cache, block_table, seq_lens, max_seq_len: int,
@@ -385,14 +435,21 @@ def decode_attention_scored(preset: int, query, kv_cache, block_table, seq_lens,
                             doc_start=None) -> None:
     """tq_decode_attention_scored on torch tensors.  query (B, Hq, D) contiguous; alibi_slopes float32 (Hq,);
     doc_start int32 (B,); workspace as scored_workspace_bytes says."""
-    fn = "decode_attention_scored"
-    args = _scored_args(fn, preset, query, kv_cache, block_table, seq_lens, max_seq_len, num_kv_heads, block_size,
-                        signs, centroids, out, lse, workspace, num_splits, softmax_scale, softcap, alibi_slopes,
-                        window, prefix, doc_start)
-    with _Device(query.device, stream) as st:
-        rc = tq_decode_attention_scored(*args, st)
-    if rc:
-        raise TQError("tq_decode_attention_scored", rc)
+    dev, args = _scored_args("decode_attention_scored", preset, query, kv_cache, block_table, seq_lens, max_seq_len,
+                             num_kv_heads, block_size, signs, centroids, out, lse, workspace, num_splits,
+                             softmax_scale, softcap, alibi_slopes, window, prefix, doc_start)
+    _enqueue("tq_decode_attention_scored", dev, stream, args)
+
+
+def _acc_ok(acc, dev: int, B, Hk) -> bool:
+    return (acc.get_device() == dev and acc.dtype is _dtypes()["f32"] and acc.dim() == 3 and acc.shape[0] == B
+            and acc.shape[1] == Hk and _rows_ok(acc))
+
+
+def _acc_refusal(fn, acc, dev: int, B, Hk, T=None):
+    _on(acc, dev, (_dtypes()["f32"],), (B, Hk, None), fn, "acc", contiguous=False)
+    _need(_rows_ok(acc), fn, "acc rows are not contiguous")
+    raise ValueError(f"{fn}: acc rows hold {acc.shape[2]} tokens, max_seq_len is {T}")
 
 
 def decode_attention_weights(preset: int, query, kv_cache, block_table, seq_lens, max_seq_len: int,
@@ -403,39 +460,37 @@ def decode_attention_weights(preset: int, query, kv_cache, block_table, seq_lens
     """tq_decode_attention_weights on torch tensors: decode_attention_scored that also adds every visible
     token's attention weight to acc, float32 (B, Hk, T) with T >= max_seq_len and contiguous rows.
     lse may be None; workspace as scored_workspace_bytes(..., weights=True) says."""
-    import torch
     fn = "decode_attention_weights"
-    args = _scored_args(fn, preset, query, kv_cache, block_table, seq_lens, max_seq_len, num_kv_heads, block_size,
-                        signs, centroids, out, lse, workspace, num_splits, softmax_scale, softcap, alibi_slopes,
-                        window, prefix, doc_start)
-    _on(acc, query.device, (torch.float32,), (query.shape[0], int(num_kv_heads), None), fn, "acc", contiguous=False)
-    _need(acc.shape[2] >= int(max_seq_len), fn, f"acc rows hold {acc.shape[2]} tokens, max_seq_len is {max_seq_len}")
-    _need(acc.shape[2] <= 1 or acc.stride(2) == 1, fn, "acc rows are not contiguous")
-    with _Device(query.device, stream) as st:
-        rc = tq_decode_attention_weights(*args, _ptr(acc), *_acc_strides(acc), st)
-    if rc:
-        raise TQError("tq_decode_attention_weights", rc)
+    dev, args = _scored_args(fn, preset, query, kv_cache, block_table, seq_lens, max_seq_len, num_kv_heads, block_size,
+                             signs, centroids, out, lse, workspace, num_splits, softmax_scale, softcap, alibi_slopes,
+                             window, prefix, doc_start)
+    if not (_acc_ok(acc, dev, args[2], args[4]) and acc.shape[2] >= max_seq_len):
+        _acc_refusal(fn, acc, dev, args[2], args[4], max_seq_len)
+    _enqueue("tq_decode_attention_weights", dev, stream, args + (acc.data_ptr(), *_acc_strides(acc)))
 
 
 def evict_select(acc, seq_lens, max_seq_len: int, budget: int, keep, new_lens, prefix: int = 0, recent: int = 0,
                  stream=None) -> None:
     """tq_evict_select on torch tensors: acc float32 (B, Hk, T), T >= max_seq_len, contiguous rows; keep int32
     (B, Hk, budget) and new_lens int32 (B,) are written."""
-    import torch
-    fn = "evict_select"
-    dev = acc.device
-    _on(acc, dev, (torch.float32,), (None, None, None), fn, "acc", contiguous=False)
+    fn, i32 = "evict_select", _dtypes()["i32"]
+    _need(isinstance(acc, _dtypes()["tensor"]) and acc.is_cuda and acc.dim() == 3, fn,
+          "acc is not a (B, Hk, T) tensor of a GPU")
+    dev = acc.get_device()
+    max_seq_len, budget = int(max_seq_len), int(budget)
     B, Hk, T = acc.shape
-    _need(T >= int(max_seq_len), fn, f"acc rows hold {T} tokens, max_seq_len is {max_seq_len}")
-    _need(T <= 1 or acc.stride(2) == 1, fn, "acc rows are not contiguous")
-    _on(seq_lens, dev, (torch.int32,), (B,), fn, "seq_lens")
-    _on(keep, dev, (torch.int32,), (B, Hk, int(budget)), fn, "keep")
-    _on(new_lens, dev, (torch.int32,), (B,), fn, "new_lens")
-    with _Device(dev, stream) as st:
-        rc = tq_evict_select(B, Hk, _ptr(acc), *_acc_strides(acc), _ptr(seq_lens), int(max_seq_len), int(budget),
-                             int(prefix), int(recent), _ptr(keep), _ptr(new_lens), st)
-    if rc:
-        raise TQError("tq_evict_select", rc)
+    if not (_acc_ok(acc, dev, B, Hk) and T >= max_seq_len):
+        _acc_refusal(fn, acc, dev, B, Hk, max_seq_len)
+    if not (seq_lens.get_device() == dev and seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.is_contiguous()
+            and keep.get_device() == dev and keep.dtype is i32 and keep.shape == (B, Hk, budget) and keep.is_contiguous()
+            and new_lens.get_device() == dev and new_lens.dtype is i32 and new_lens.shape == (B,)
+            and new_lens.is_contiguous()):
+        _on(seq_lens, dev, (i32,), (B,), fn, "seq_lens")
+        _on(keep, dev, (i32,), (B, Hk, budget), fn, "keep")
+        _on(new_lens, dev, (i32,), (B,), fn, "new_lens")
+    _enqueue("tq_evict_select", dev, stream,
+             (B, Hk, acc.data_ptr(), *_acc_strides(acc), seq_lens.data_ptr(), max_seq_len, budget, int(prefix), int(recent),
+              keep.data_ptr(), new_lens.data_ptr()))
 
 
 def evict_compact(preset: int, keep, seq_lens, kv_cache, block_table, num_kv_heads: int, block_size: int, acc=None,
@@ -443,27 +498,36 @@ def evict_compact(preset: int, keep, seq_lens, kv_cache, block_table, num_kv_hea
     """tq_evict_compact on torch tensors: the slots keep (int32 (B, Hk, budget)) names move to the front of their
     sequences in kv_cache, and the running sums acc (float32 (B, Hk, T)) with them.  seq_lens: the lengths
     before the eviction; sequences longer than the table or acc covers are left alone."""
-    import torch
-    fn = "evict_compact"
-    dev = kv_cache.device
-    _on(keep, dev, (torch.int32,), (None, int(num_kv_heads), None), fn, "keep")
-    B, Hk, budget = keep.shape
-    _table_and_lens(fn, dev, block_table, seq_lens, B)
-    _need(B <= 1 or block_table.stride(0) >= block_table.shape[1], fn, "block_table rows overlap")
-    slot = tq_get_layout(int(preset), 128)["slot_size_aligned"]
-    _on(kv_cache, dev, (torch.uint8,), (None, int(block_size), Hk, slot), fn, "kv_cache")
-    max_len = min(block_table.shape[1] * int(block_size), 1 << 30)
-    strides = (0, 0)
+    fn, dt = "evict_compact", _dtypes()
+    i32 = dt["i32"]
+    _need(isinstance(kv_cache, dt["tensor"]) and kv_cache.is_cuda, fn, "kv_cache is not a tensor of a GPU")
+    dev = kv_cache.get_device()
+    preset, num_kv_heads, block_size = int(preset), int(num_kv_heads), int(block_size)
+    slot = _slot_of(preset, 128)[0]
+    B = block_table.shape[0]
+    if not (kv_cache.dtype is dt["u8"] and kv_cache.shape[1:] == (block_size, num_kv_heads, slot)
+            and kv_cache.is_contiguous()
+            and keep.get_device() == dev and keep.dtype is i32 and keep.dim() == 3
+            and keep.shape[:2] == (B, num_kv_heads) and keep.is_contiguous()
+            and block_table.get_device() == dev and block_table.dtype is i32 and block_table.dim() == 2
+            and _rows_ok(block_table) and (B <= 1 or block_table.stride(0) >= block_table.shape[1])
+            and seq_lens.get_device() == dev and seq_lens.dtype is i32 and seq_lens.shape == (B,)
+            and seq_lens.is_contiguous()):
+        _on(kv_cache, dev, (dt["u8"],), (None, block_size, num_kv_heads, slot), fn, "kv_cache")
+        _on(block_table, dev, (i32,), (None, None), fn, "block_table", contiguous=False)
+        _need(_rows_ok(block_table), fn, "block_table rows are not contiguous")
+        _need(B <= 1 or block_table.stride(0) >= block_table.shape[1], fn, "block_table rows overlap")
+        _on(keep, dev, (i32,), (B, num_kv_heads, None), fn, "keep")
+        _on(seq_lens, dev, (i32,), (B,), fn, "seq_lens")
+    max_len, budget = min(block_table.shape[1] * block_size, 1 << 30), keep.shape[2]
+    a = (None, 0, 0)
     if acc is not None:
-        _on(acc, dev, (torch.float32,), (B, Hk, None), fn, "acc", contiguous=False)
-        _need(acc.shape[2] <= 1 or acc.stride(2) == 1, fn, "acc rows are not contiguous")
-        max_len, strides = min(max_len, acc.shape[2]), _acc_strides(acc)
-    with _Device(dev, stream) as st:
-        rc = tq_evict_compact(int(preset), 128, B, Hk, int(block_size), _ptr(kv_cache), kv_cache.shape[0],
-                              _ptr(block_table), block_table.stride(0), _ptr(keep), budget, _ptr(seq_lens), max_len,
-                              _ptr(acc), *strides, st)
-    if rc:
-        raise TQError("tq_evict_compact", rc)
+        if not _acc_ok(acc, dev, B, num_kv_heads):
+            _acc_refusal(fn, acc, dev, B, num_kv_heads)
+        max_len, a = min(max_len, acc.shape[2]), (acc.data_ptr(), *_acc_strides(acc))
+    _enqueue("tq_evict_compact", dev, stream,
+             (preset, 128, B, num_kv_heads, block_size, kv_cache.data_ptr(), kv_cache.shape[0], block_table.data_ptr(),
+              block_table.stride(0), keep.data_ptr(), budget, seq_lens.data_ptr(), max_len, *a))
 
 
 TQ_NOALLOC_SCRATCH_BYTES = 16 << 20
