@@ -327,14 +327,26 @@ typedef struct {
     const int32_t* doc_start;
 } tq_score_mods;
 
+/* Split count the scored decode uses for num_splits = 0: as
+ * tq_decode_pick_splits for the longest visible length, down to 32 tokens a
+ * split.  Returns as there. */
+int tq_decode_scored_pick_splits(int preset, int head_dim, int batch, int num_q_heads, int num_kv_heads,
+                                 int max_seq_len, int window, int prefix);
+
+/* Bytes of caller-owned workspace of tq_decode_attention_scored: the split
+ * partials and where each sequence's lie.  0 for sizes out of range. */
+size_t tq_decode_scored_workspace_bytes(int batch, int num_q_heads, int num_splits, int head_dim);
+
 /* tq_decode_attention with score modifiers; mods NULL (or all zero) is
- * tq_decode_attention exactly.  num_splits = 0 picks as tq_decode_pick_splits
- * does for the longest visible length, 32 * T tokens with T the smaller of
- * ceil(max_seq_len / 32) and, with a window, window / 32 + 2 (+ prefix / 32 + 2
- * when prefix > 0), but at most max_seq_len.  The splits share the 32-token
- * tiles that hold visible tokens.  Other arguments, results, errors and
- * supported shapes as tq_decode_attention; TQ_ERR_INVALID_ARG for modifiers out
- * of range or max_seq_len above 2^30. */
+ * tq_decode_attention exactly (also in the workspace it needs).  num_splits = 0
+ * picks as tq_decode_scored_pick_splits does.  The splits share the 32-token
+ * tiles that hold visible tokens: batch * num_splits splits of one size, given
+ * out to the sequences by their visible lengths (batches above 512 sequences:
+ * num_splits for each).
+ * workspace: >= tq_decode_scored_workspace_bytes for the split count used.
+ * Other arguments, results, errors and supported shapes as
+ * tq_decode_attention; TQ_ERR_INVALID_ARG for modifiers out of range or
+ * max_seq_len above 2^30. */
 int tq_decode_attention_scored(int preset, int head_dim, int batch, int num_q_heads,
                                int num_kv_heads, int block_size, int q_dtype, const void* query,
                                const uint8_t* kv_cache, long long num_blocks,
@@ -344,8 +356,8 @@ int tq_decode_attention_scored(int preset, int head_dim, int batch, int num_q_he
                                void* out, int out_dtype, float* lse, void* workspace,
                                size_t workspace_bytes, const tq_score_mods* mods, void* stream);
 
-/* Bytes of caller-owned workspace of tq_decode_attention_weights: the split
- * partials, an lse per query head and the scores of every listed token, about
+/* Bytes of caller-owned workspace of tq_decode_attention_weights: that of
+ * the scored decode and the scores of every listed token, about
  * 4 * num_q_heads bytes per visible token.  0 for sizes out of range. */
 size_t tq_decode_weights_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
                                          int num_splits, int head_dim, int max_seq_len,

@@ -10,7 +10,8 @@ from . import _lib
 from ._lib import (PRESETS, TQ_2BIT_NC, TQ_3BIT_NC, TQ_4BIT_NC, TQ_LAYOUT_SOA, TQ_BF16, TQ_F16, TQ_F32, TQ_K3V4_NC,
                    TQ_K8V4, TQError, TQScoreMods, decode_attention, decode_attention_scored, decode_attention_weights,
                    dequant, evict_compact, evict_select, scored_workspace_bytes, tq_decode_attention_scored,
-                   tq_decode_attention_weights, tq_decode_weights_workspace_bytes, tq_evict_compact, tq_evict_select, load, store, tq_build_codebook,
+                   tq_decode_attention_weights, tq_decode_scored_pick_splits, tq_decode_scored_workspace_bytes,
+                   tq_decode_weights_workspace_bytes, tq_evict_compact, tq_evict_select, load, store, tq_build_codebook,
                    tq_decode_attention, tq_decode_kernel_kind, tq_decode_pick_splits, tq_decode_workspace_bytes,
                    tq_decode_attention_sparse_v, tq_dequant, tq_get_layout, tq_make_signs, tq_status_string, tq_store, tq_version)
 
@@ -19,7 +20,7 @@ __all__ = ["PRESETS", "TQ_K8V4", "TQ_4BIT_NC", "TQ_K3V4_NC", "TQ_3BIT_NC", "TQ_2
            "tq_decode_attention", "tq_decode_attention_sparse_v", "tq_dequant", "tq_decode_kernel_kind", "tq_get_layout", "tq_build_codebook", "tq_make_signs",
            "TQScoreMods", "decode_attention_scored", "decode_attention_weights", "evict_select", "evict_compact",
            "scored_workspace_bytes", "tq_decode_attention_scored", "tq_decode_attention_weights",
-           "tq_decode_weights_workspace_bytes", "tq_evict_select", "tq_evict_compact",
+           "tq_decode_scored_pick_splits", "tq_decode_scored_workspace_bytes", "tq_decode_weights_workspace_bytes", "tq_evict_select", "tq_evict_compact",
            "tq_decode_workspace_bytes", "tq_decode_pick_splits", "tq_status_string", "tq_version"]
 
 SIGN_SEED = 42          # per-layer seed = 42 + 1337 * layer

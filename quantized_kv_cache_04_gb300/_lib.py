@@ -91,6 +91,9 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                                              _c_vp, _c_sz, ctypes.POINTER(TQScoreMods), _c_vp])
     L.tq_decode_attention_weights.argtypes = (L.tq_decode_attention_scored.argtypes[:-1]
                                               + [_c_vp, _c_ll, _c_ll, _c_vp])
+    L.tq_decode_scored_pick_splits.argtypes = [_c_int] * 8
+    L.tq_decode_scored_workspace_bytes.argtypes = [_c_int] * 4
+    L.tq_decode_scored_workspace_bytes.restype = _c_sz
     L.tq_decode_weights_workspace_bytes.argtypes = [_c_int] * 8
     L.tq_decode_weights_workspace_bytes.restype = _c_sz
     L.tq_evict_select.argtypes = ([_c_int] * 2 + [_c_vp, _c_ll, _c_ll, _c_vp] + [_c_int] * 4
@@ -189,6 +192,20 @@ def tq_decode_attention_scored(*args) -> int:
 def tq_decode_attention_weights(*args) -> int:
     """Raw C call; arguments exactly as in include/tq.h.  Returns the status."""
     return load().tq_decode_attention_weights(*args)
+
+
+def tq_decode_scored_pick_splits(preset: int, head_dim: int, batch: int, num_q_heads: int, num_kv_heads: int,
+                                 max_seq_len: int, window: int = 0, prefix: int = 0) -> int:
+    s = load().tq_decode_scored_pick_splits(int(preset), int(head_dim), int(batch), int(num_q_heads),
+                                            int(num_kv_heads), int(max_seq_len), int(window), int(prefix))
+    if s < 0:
+        raise TQError("tq_decode_scored_pick_splits", s)
+    return s
+
+
+def tq_decode_scored_workspace_bytes(batch: int, num_q_heads: int, num_splits: int, head_dim: int = 128) -> int:
+    return int(load().tq_decode_scored_workspace_bytes(int(batch), int(num_q_heads), int(num_splits),
+                                                       int(head_dim)))
 
 
 def tq_decode_weights_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, num_splits: int,
@@ -329,26 +346,18 @@ def _enqueue(name: str, dev: int, stream, args) -> None:
         raise TQError(name, rc)
 
 
-def _listed_len(max_seq_len: int, window: int, prefix: int) -> int:
-    """The longest visible length num_splits = 0 is picked for (include/tq.h)."""
-    if window <= 0:
-        return max_seq_len
-    some = window // 32 + 2 + (prefix // 32 + 2 if prefix > 0 else 0)
-    return min(max_seq_len, 32 * min((max_seq_len + 31) // 32, some))
-
-
 def scored_workspace_bytes(preset: int, batch: int, num_q_heads: int, num_kv_heads: int, max_seq_len: int,
                            window: int = 0, prefix: int = 0, weights: bool = False, num_splits: int = 0,
                            head_dim: int = 128) -> int:
     """Workspace bytes of decode_attention_scored, or with `weights` of decode_attention_weights, for the
     split count given or the one the library picks."""
-    S = int(num_splits) or tq_decode_pick_splits(preset, head_dim, batch, num_q_heads, num_kv_heads,
-                                                 _listed_len(int(max_seq_len), int(window), int(prefix)))
+    S = int(num_splits) or tq_decode_scored_pick_splits(preset, head_dim, batch, num_q_heads, num_kv_heads,
+                                                        max_seq_len, window, prefix)
     if weights:
         n = tq_decode_weights_workspace_bytes(batch, num_q_heads, num_kv_heads, S, head_dim, max_seq_len,
                                               window, prefix)
     else:
-        n = tq_decode_workspace_bytes(batch, num_q_heads, S, head_dim)
+        n = tq_decode_scored_workspace_bytes(batch, num_q_heads, S, head_dim)
     return max(16, n)
 
 

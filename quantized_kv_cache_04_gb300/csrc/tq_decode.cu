@@ -30,7 +30,9 @@ namespace {
 // data, or met a block-table entry outside the cache) makes the row NaN.
 constexpr int kStage2Warps = 8;
 
-template <typename TO>
+// SCORED: the splits of sequence b are those of its plan (SplitPlan), a partial
+// per split and query head.
+template <typename TO, bool SCORED>
 __global__ void __launch_bounds__(32 * kStage2Warps) stage2_kernel(DecodeArgs a, int R)
 {
     __shared__ float s_part[kStage2Warps][kHeadDim + 2];
@@ -42,18 +44,25 @@ __global__ void __launch_bounds__(32 * kStage2Warps) stage2_kernel(DecodeArgs a,
     const int r = warp % R;                                    // this warp's share of the splits
     const long long bh = (long long)blockIdx.x * rows_per_cta + warp / R;   // b * Hq + hq
     const bool live = bh < (long long)a.B * a.Hq;
-    const int S = a.num_splits;
+    int S = a.num_splits;
     constexpr int kRound = 16;
     float M = -INFINITY, W = 0.f;
     float o[4] = {0.f, 0.f, 0.f, 0.f};
     if (live) {
         const float* mp = a.mid + bh * S * (kHeadDim + 1);
+        long long stride = kHeadDim + 1;             // from one split's partial to the next
+        if constexpr (SCORED) {
+            const int b = int(bh / a.Hq);
+            S = a.mods.plan[2 * b + 1];
+            mp = a.mid + ((long long)a.mods.plan[2 * b] * a.Hq + bh % a.Hq) * (kHeadDim + 1);
+            stride = (long long)a.Hq * (kHeadDim + 1);
+        }
         for (int s0 = r; s0 < S; s0 += kRound * R) {
             float ls[kRound], x[kRound][4];
 #pragma unroll
             for (int u = 0; u < kRound; ++u) {
                 const int sp = s0 + u * R;
-                const float* row = mp + min(sp, S - 1) * (kHeadDim + 1);
+                const float* row = mp + min(sp, S - 1) * stride;
                 ls[u] = sp < S ? row[kHeadDim] : -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[u][i] = row[4 * lane + i];
@@ -121,7 +130,7 @@ __global__ void __launch_bounds__(32 * kStage2Warps) stage2_kernel(DecodeArgs a,
     if (lane == 0 && a.lse) a.lse[bh] = M == -INFINITY ? -INFINITY : M + logf(W);
 }
 
-template <typename TO>
+template <typename TO, bool SCORED>
 cudaError_t launch_stage2(const DecodeArgs& a, cudaStream_t st)
 {
     int R = (a.num_splits + 15) / 16;                 // warps per row: at most 16 splits each
@@ -137,7 +146,13 @@ cudaError_t launch_stage2(const DecodeArgs& a, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, stage2_kernel<TO>, a, R);
+    return cudaLaunchKernelEx(&cfg, stage2_kernel<TO, SCORED>, a, R);
+}
+
+template <typename TO>
+cudaError_t launch_stage2(const DecodeArgs& a, bool scored, cudaStream_t st)
+{
+    return scored ? launch_stage2<TO, true>(a, st) : launch_stage2<TO, false>(a, st);
 }
 
 template <bool FP8, int KB, int VB>
@@ -200,7 +215,8 @@ void stage1_shape(const tq_layout& L, bool soa, int Hk, int G, int* cps, int* sl
 
 }  // namespace
 
-int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int num_kv_heads, int max_seq_len)
+int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int num_kv_heads, int max_seq_len,
+                int min_split)
 {
     if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || max_seq_len <= 0) return 1;
     int cps = 1, slots = 1;
@@ -208,9 +224,9 @@ int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int nu
     // Critical path of stage 1 in 32-token tiles: the CTAs of all splits run
     // in ceil(CTAs / slots) waves, each as long as one split's tiles plus a
     // fixed start-up (q preparation, first copy latency, epilogue) worth about
-    // kStartTiles tiles.  Splits shorter than 128 tokens are not used.
+    // kStartTiles tiles.  Splits shorter than min_split tokens are not used.
     constexpr double kStartTiles = 3.0;
-    long long max_s = (max_seq_len + 127) / 128;
+    long long max_s = ((long long)max_seq_len + min_split - 1) / min_split;
     if (max_s > TQ_MAX_SPLITS) max_s = TQ_MAX_SPLITS;
     if (max_s < 1) max_s = 1;
     int best = 1;
@@ -235,6 +251,15 @@ namespace {
 bool mods_ok(const tq_score_mods& m)
 {
     return m.softcap >= 0.f && m.softcap <= 3.0e38f && m.window >= 0 && m.prefix >= 0;
+}
+
+// Split count of a scored decode, for the longest visible length.  Down to one
+// 32-token tile per split: with few sequences a tile more costs a split more
+// than merging its partial does (one sequence of 2047 tokens, 8 kv heads: 22.6 us
+// with 16 splits, 20.5 with 32, 18.5 with 64).
+int pick_scored_splits(const tq_layout& L, bool soa, int batch, int Hq, int Hk, int max_len, int window, int prefix)
+{
+    return pick_splits(L, soa, batch, Hq, Hk, std::min(max_len, 32 * visible_tiles(max_len, window, prefix)), 32);
 }
 
 // Where a call that accumulates attention weights adds them.
@@ -272,12 +297,12 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
     if (reinterpret_cast<uintptr_t>(workspace) & 15) return TQ_ERR_INVALID_ARG;
     const bool soa = is_soa(preset);
     const int G = num_q_heads / num_kv_heads;
-    const int listed = mods ? std::min(max_seq_len, 32 * visible_tiles(max_seq_len, mods->window, mods->prefix))
-                            : max_seq_len;
-    const int S = num_splits ? num_splits : pick_splits(L, soa, batch, num_q_heads, num_kv_heads, listed);
-    if (workspace_bytes < (wout ? tq_decode_weights_workspace_bytes(batch, num_q_heads, num_kv_heads, S, head_dim,
-                                                                    max_seq_len, mods->window, mods->prefix)
-                                : tq_decode_workspace_bytes(batch, num_q_heads, S, head_dim)))
+    const int S = num_splits ? num_splits
+                  : mods ? pick_scored_splits(L, soa, batch, num_q_heads, num_kv_heads, max_seq_len, mods->window, mods->prefix)
+                         : pick_splits(L, soa, batch, num_q_heads, num_kv_heads, max_seq_len);
+    ScoredLayout lay = {};
+    if (mods) lay = scored_layout(batch, num_q_heads, num_kv_heads, S, max_seq_len, mods->window, mods->prefix, wout != nullptr);
+    if (workspace_bytes < (mods ? lay.bytes : tq_decode_workspace_bytes(batch, num_q_heads, S, head_dim)))
         return TQ_ERR_WORKSPACE;
     if (wout &&
         (!wout->acc || !acc_strides_ok(batch, num_kv_heads, wout->stride_b, wout->stride_h, max_seq_len)))
@@ -313,17 +338,15 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
         a.mods.prefix = mods->prefix;
         a.mods.doc_start = mods->doc_start;
         a.mods.max_len = wout ? max_seq_len : kMaxListedLen;
-    }
-    if (wout) {
-        // after the partials: an lse per query head (used when the caller
-        // wants none), then the scores
-        const WeightsLayout w = weights_layout(batch, num_q_heads, num_kv_heads, S, max_seq_len, mods->window,
-                                               mods->prefix);
+        a.mods.B = batch;
         char* ws = static_cast<char*>(workspace);
-        if (!a.lse) a.lse = reinterpret_cast<float*>(ws + w.off_lse);
-        a.mods.scores = reinterpret_cast<float*>(ws + w.off_scores);
-        a.mods.vtok = w.vtok;
-        a.mods.gp = score_heads(G);
+        a.mods.plan = reinterpret_cast<int*>(ws + lay.off_plan);
+        if (wout) {
+            if (!a.lse) a.lse = reinterpret_cast<float*>(ws + lay.off_lse);
+            a.mods.scores = reinterpret_cast<float*>(ws + lay.off_scores);
+            a.mods.vtok = lay.vtok;
+            a.mods.gp = score_heads(G);
+        }
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
 
@@ -342,13 +365,12 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
                                           : launch_stage1<__nv_bfloat16, false>(preset, a, st);
         if (e != cudaSuccess) return TQ_ERR_CUDA;
     }
-    const cudaError_t e2 = out_dtype == TQ_F32 ? launch_stage2<float>(a, st)
-                           : out_dtype == TQ_F16 ? launch_stage2<__half>(a, st)
-                                                 : launch_stage2<__nv_bfloat16>(a, st);
+    const cudaError_t e2 = out_dtype == TQ_F32   ? launch_stage2<float>(a, mods != nullptr, st)
+                           : out_dtype == TQ_F16 ? launch_stage2<__half>(a, mods != nullptr, st)
+                                                 : launch_stage2<__nv_bfloat16>(a, mods != nullptr, st);
     if (e2 != cudaSuccess) return TQ_ERR_CUDA;
-    if (wout &&
-        launch_weights(a.mods, seq_lens, a.lse, wout->acc, wout->stride_b, wout->stride_h, batch, num_kv_heads, G, st) !=
-            cudaSuccess)
+    if (wout && launch_weights(a.mods, seq_lens, a.lse, wout->acc, wout->stride_b, wout->stride_h, num_kv_heads, G, st) !=
+                    cudaSuccess)
         return TQ_ERR_CUDA;
     return TQ_OK;
 }
@@ -405,6 +427,19 @@ extern "C" int tq_decode_attention(int preset, int head_dim, int batch, int num_
                                         block_table_stride, seq_lens, max_seq_len, softmax_scale,
                                         num_splits, signs, centroids, out, out_dtype, lse, workspace,
                                         workspace_bytes, 0.f, stream);
+}
+
+extern "C" int tq_decode_scored_pick_splits(int preset, int head_dim, int batch, int num_q_heads, int num_kv_heads,
+                                            int max_seq_len, int window, int prefix)
+{
+    using namespace tq;
+    tq_layout L;
+    const int rc = fill_layout(preset, head_dim, &L);
+    if (rc) return rc;
+    if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads || max_seq_len > kMaxListedLen || window < 0 ||
+        prefix < 0)
+        return TQ_ERR_INVALID_ARG;
+    return pick_scored_splits(L, is_soa(preset), batch, num_q_heads, num_kv_heads, std::max(max_seq_len, 0), window, prefix);
 }
 
 extern "C" int tq_decode_attention_scored(int preset, int head_dim, int batch, int num_q_heads,

@@ -67,13 +67,29 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int lane, int (&c)[
 template <typename TQ, bool KEY_FP8, int KBITS, int VBITS, int GM, bool SCORED>
 __global__ void __launch_bounds__(kWarps * 32) stage1_kernel(DecodeArgs a)
 {
-    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int h = blockIdx.y;
+    int split = blockIdx.x, b = blockIdx.z, chunk = 0;
+    // scored: the launch's splits go by the plan of the batch (SplitPlan)
+    [[maybe_unused]] int id = 0;
+    if constexpr (SCORED) {
+        __shared__ int s_plan[kPlanMax + 4];
+        id = blockIdx.z * a.num_splits + blockIdx.x;
+        const SplitPlan plan(a.mods, a.seq_lens, a.num_splits, id, blockIdx.x + blockIdx.y + blockIdx.z == 0, s_plan);
+        if (plan.b < 0) return;
+        b = plan.b;
+        split = id - plan.base;
+        chunk = 32 * plan.chunk;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.G, S = a.num_splits;
     const int L = a.seq_lens[b];
     [[maybe_unused]] VisibleSet vis(SCORED ? a.mods : ScoreArgs{}, SCORED ? min(L, a.mods.max_len) : 0, b);
     const int n = SCORED ? 32 * vis.tiles() : L;     // positions the splits share
-    const int chunk = (n + S - 1) / S;
+    if constexpr (!SCORED) chunk = (n + S - 1) / S;
+    // this split's partial of query head hq
+    auto partial = [&](int hq) {
+        return a.mid + (SCORED ? (long long)id * a.Hq + hq : ((long long)b * a.Hq + hq) * S + split) * (kHeadDim + 1);
+    };
     const int t0 = split * chunk;
     const int t1 = min(n, t0 + chunk);
     const bool too_long = SCORED && L > a.mods.max_len;   // past what can be listed
@@ -85,8 +101,7 @@ __global__ void __launch_bounds__(kWarps * 32) stage1_kernel(DecodeArgs a)
     if (t0 >= t1 || too_long) {   // empty split: lse = -inf (too long: NaN), zero partial output
         for (int i = threadIdx.x; i < G * (kHeadDim + 1); i += blockDim.x) {
             const int g = i / (kHeadDim + 1), d = i % (kHeadDim + 1);
-            float* m = a.mid + (((long long)b * a.Hq + h * G + g) * S + split) * (kHeadDim + 1);
-            m[d] = d == kHeadDim ? (too_long ? __int_as_float(0x7fc00000) : -INFINITY) : 0.f;
+            partial(h * G + g)[d] = d == kHeadDim ? (too_long ? __int_as_float(0x7fc00000) : -INFINITY) : 0.f;
         }
         return;
     }
@@ -164,9 +179,9 @@ __global__ void __launch_bounds__(kWarps * 32) stage1_kernel(DecodeArgs a)
 
         if constexpr (SCORED) {
             float mine = 0.f;                // the score this lane writes (query head `lane`)
+            if (a.mods.cap > 0.f) softcap_warp(s, a.mods.cap, a.mods.inv_cap);
 #pragma unroll
             for (int g = 0; g < GM; ++g) {
-                if (a.mods.cap > 0.f) s[g] = a.mods.cap * tanhf(s[g] * a.mods.inv_cap);
                 if (a.mods.slopes && g < G) s[g] = fmaf(-a.mods.slopes[h * G + g], float(L - 1 - t), s[g]);
                 if (lane == g) mine = s[g];
             }
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32) stage1_kernel(DecodeArgs a)
             lsum += s_l[w][g] * f;
             o += s_acc[w][g][d] * f;
         }
-        float* mp = a.mid + (((long long)b * a.Hq + h * G + g) * S + split) * (kHeadDim + 1);
+        float* mp = partial(h * G + g);
         mp[d] = SCORED && lsum == 0.f ? 0.f : o / lsum;      // a split may list no visible token
         if (d == 0) mp[kHeadDim] = s_bad ? __int_as_float(0x7fc00000) : M + logf(lsum);
     }

@@ -654,9 +654,20 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int ngroups = a.Hk / a.hpc;
     const int kvg = blockIdx.x % ngroups;     // which hpc kv heads
     const int qg = (blockIdx.x / ngroups) % a.nqg;   // which 8 query heads of each kv head (G > 8)
-    const int split = blockIdx.x / ngroups / a.nqg;
-    const int b = a.lpt ? seq_of_rank(a.seq_lens, gridDim.y, blockIdx.y, reinterpret_cast<int*>(smem))
-                        : blockIdx.y;
+    int split = blockIdx.x / ngroups / a.nqg, b, chunk;
+    // scored: the launch's splits go by the plan of the batch (SplitPlan)
+    [[maybe_unused]] int id = 0;
+    if constexpr (SCORED) {
+        id = blockIdx.y * a.num_splits + split;
+        const SplitPlan plan(a.mods, a.seq_lens, a.num_splits, id, blockIdx.x == 0 && blockIdx.y == 0,
+                             reinterpret_cast<int*>(smem));
+        if (plan.b < 0) return;
+        b = plan.b;
+        split = id - plan.base;
+        chunk = plan.chunk * kTile;
+    } else {
+        b = a.lpt ? seq_of_rank(a.seq_lens, gridDim.y, blockIdx.y, reinterpret_cast<int*>(smem)) : blockIdx.y;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3;
     const int h0 = kvg * a.hpc;               // first kv head of this CTA
@@ -670,17 +681,21 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int nwarps = blockDim.x >> 5;
 
     const int L = a.seq_lens[b];
-    int chunk = (L + S - 1) / S;
-    chunk = (chunk + kTile - 1) / kTile * kTile;
+    if constexpr (!SCORED) {
+        chunk = (L + S - 1) / S;
+        chunk = (chunk + kTile - 1) / kTile * kTile;
+    }
+    // this split's partial of query head hq
+    auto partial = [&](int hq) {
+        return a.mid + (SCORED ? (long long)id * Hq + hq : ((long long)b * Hq + hq) * S + split) * (kHeadDim + 1);
+    };
     int t_begin = split * chunk;
     int t_end = min(L, t_begin + chunk);
-    // scored: the splits share the tiles that hold visible tokens; t_begin and
-    // t_end are then positions in that list (32 per tile)
+    // scored: t_begin and t_end are positions in the list of tiles that hold
+    // visible tokens (32 per tile)
     bool too_long = false;       // past what can be listed: a NaN lse, nothing read
     [[maybe_unused]] VisibleSet vis(SCORED ? a.mods : ScoreArgs{}, SCORED ? min(L, a.mods.max_len) : 0, b);
     if constexpr (SCORED) {
-        chunk = (vis.tiles() + S - 1) / S * kTile;
-        t_begin = split * chunk;
         t_end = min(vis.tiles() * kTile, t_begin + chunk);
         too_long = L > a.mods.max_len;
     }
@@ -688,12 +703,11 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     if (t_begin >= t_end || a.num_blocks <= 0 || (SCORED && too_long)) {
         // empty split: lse = -inf and a zero partial; tokens but no cache
         // block to read them from: a NaN lse
-        const float lse0 = t_begin >= t_end ? -INFINITY : __int_as_float(0x7fc00000);
+        const float lse0 = t_begin >= t_end && !too_long ? -INFINITY : __int_as_float(0x7fc00000);
         for (int i = threadIdx.x; i < Hc * Greal * (kHeadDim + 1); i += blockDim.x) {
             const int r = i / (kHeadDim + 1), d = i % (kHeadDim + 1);
             const int hq = (h0 + r / Greal) * Gall + qh0 + r % Greal;
-            float* m = a.mid + (((long long)b * Hq + hq) * S + split) * (kHeadDim + 1);
-            m[d] = d == kHeadDim ? lse0 : 0.f;
+            partial(hq)[d] = d == kHeadDim ? lse0 : 0.f;
         }
         return;
     }
@@ -1063,11 +1077,14 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             // softcap, then the distance bias (distance: to the newest token)
             if (a.mods.cap > 0.f) {
 #pragma unroll
-                for (int j = 0; j < NH; ++j)
-#pragma unroll
-                    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) s[j][rt][r] = cap2 * tanhf(s[j][rt][r] * inv_cap2);
+                for (int j = 0; j < NH; ++j) {
+                    float x[4] = {s[j][0][0], s[j][0][1], s[j][1][0], s[j][1][1]};
+                    softcap_warp(x, cap2, inv_cap2);
+                    s[j][0][0] = x[0];
+                    s[j][0][1] = x[1];
+                    s[j][1][0] = x[2];
+                    s[j][1][1] = x[3];
+                }
             }
             if (a.mods.slopes) {
 #pragma unroll
@@ -1253,8 +1270,7 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         __syncwarp();
         if (last && *reinterpret_cast<volatile int*>(bad_pages))
             for (int i = lane; i < Hc * Greal; i += 32)
-                a.mid[(((long long)b * Hq + (h0 + i / Greal) * Gall + qh0 + i % Greal) * S + split) *
-                          (kHeadDim + 1) + kHeadDim] = __int_as_float(0x7fc00000);
+                partial((h0 + i / Greal) * Gall + qh0 + i % Greal)[kHeadDim] = __int_as_float(0x7fc00000);
     };
     if (failed_at >= 0) {
         // let the copies that may still be in flight (tiles failed_at ..
@@ -1263,8 +1279,7 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         for (int it = failed_at; it < min(ntiles, failed_at + NST); ++it)
             mbar_wait(&full[it % NST], uint32_t((it / NST) & 1), a.wait_polls);
         if (lane < Greal)
-            a.mid[(((long long)b * Hq + h * Gall + qh0 + lane) * S + split) * (kHeadDim + 1) + kHeadDim] =
-                __int_as_float(0x7fc00000);
+            partial(h * Gall + qh0 + lane)[kHeadDim] = __int_as_float(0x7fc00000);
         finish();
     } else {
         // ---------------- epilogue: finish the row sums, write o_s and lse_s.
@@ -1282,7 +1297,7 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             const int g = G == 4 ? tig : 2 * tig + j;
             if (g >= Greal) continue;
             const int hq = h * Gall + qh0 + g;
-            float* mp = a.mid + (((long long)b * Hq + hq) * S + split) * (kHeadDim + 1);
+            float* mp = partial(hq);
             const float inv = 1.f / l_run[j];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

@@ -117,6 +117,12 @@ extern "C" size_t tq_decode_workspace_bytes(int batch, int num_q_heads, int num_
     return (size_t)batch * num_q_heads * num_splits * (head_dim + 1) * sizeof(float);
 }
 
+extern "C" size_t tq_decode_scored_workspace_bytes(int batch, int num_q_heads, int num_splits, int head_dim)
+{
+    if (batch <= 0 || num_q_heads <= 0 || num_splits <= 0 || head_dim != tq::kHeadDim) return 0;
+    return tq::scored_layout(batch, num_q_heads, 1, num_splits, 0, 0, 0, false).bytes;
+}
+
 extern "C" size_t tq_decode_weights_workspace_bytes(int batch, int num_q_heads, int num_kv_heads,
                                                     int num_splits, int head_dim, int max_seq_len,
                                                     int window, int prefix)
@@ -124,7 +130,7 @@ extern "C" size_t tq_decode_weights_workspace_bytes(int batch, int num_q_heads, 
     if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || num_splits <= 0 ||
         head_dim != tq::kHeadDim || max_seq_len < 0 || max_seq_len > tq::kMaxListedLen || window < 0 || prefix < 0)
         return 0;
-    return tq::weights_layout(batch, num_q_heads, num_kv_heads, num_splits, max_seq_len, window, prefix).bytes;
+    return tq::scored_layout(batch, num_q_heads, num_kv_heads, num_splits, max_seq_len, window, prefix, true).bytes;
 }
 
 extern "C" int tq_decode_pick_splits(int preset, int head_dim, int batch, int num_q_heads,

@@ -16,7 +16,8 @@ constexpr int kNumSMs = 152;      // GB300
 int fill_layout(int preset, int head_dim, tq_layout* L);
 // Split count for num_splits = 0 (tq_decode.cu): the one that minimises the
 // stage-1 critical path over the resident CTA slots of the kernel that runs.
-int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int num_kv_heads, int max_seq_len);
+int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int num_kv_heads, int max_seq_len,
+                int min_split = 128);
 
 inline bool block_size_ok(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 inline bool in_dtype_ok(int dt) { return dt == TQ_F16 || dt == TQ_BF16; }
@@ -105,6 +106,8 @@ struct ScoreArgs {
     int vtok;                  // listed tokens per (sequence, kv head): a multiple of 32
     int gp;                    // query heads per kv head, padded (score_heads)
     int max_len;               // sequences longer than this cannot be listed: a NaN lse
+    int B;
+    int* plan;                 // [B][2]: a sequence's first split and its number of splits
 };
 
 // columns per listed token in ScoreArgs::scores: even above 4 heads, where
@@ -122,23 +125,31 @@ inline int visible_tiles(int max_len, int window, int prefix)
     return int(all < some ? all : some);
 }
 
-// The workspace of a call that accumulates attention weights: the split
-// partials, an lse per query head, the scores; byte offsets on 256-byte
+// Workspace of a scored decode: the split partials, then for each sequence
+// where its splits begin and how many there are (SplitPlan); of one that
+// accumulates attention weights also an lse per query head (when the caller
+// takes none) and the scores.  Byte offsets on 256-byte
 // boundaries.
-struct WeightsLayout {
-    size_t off_lse, off_scores, bytes;
+struct ScoredLayout {
+    size_t off_plan, off_lse, off_scores, bytes;
     int vtok;
 };
-inline WeightsLayout weights_layout(int batch, int Hq, int Hk, int S, int max_len, int window, int prefix)
+inline ScoredLayout scored_layout(int batch, int Hq, int Hk, int S, int max_len, int window, int prefix, bool scores)
 {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    WeightsLayout w;
+    ScoredLayout w;
     w.vtok = 32 * visible_tiles(max_len, window, prefix);
-    w.off_lse = up(tq_decode_workspace_bytes(batch, Hq, S, kHeadDim));
-    w.off_scores = w.off_lse + up(size_t(batch) * Hq * sizeof(float));
-    w.bytes = w.off_scores + size_t(batch) * Hk * w.vtok * score_heads(Hq / Hk) * sizeof(float);
+    w.off_plan = up(tq_decode_workspace_bytes(batch, Hq, S, kHeadDim));
+    w.off_lse = w.off_plan + up(size_t(batch) * 2 * sizeof(int));
+    w.off_scores = w.off_lse + (scores ? up(size_t(batch) * Hq * sizeof(float)) : 0);
+    w.bytes = w.off_scores + (scores ? size_t(batch) * Hk * w.vtok * score_heads(Hq / Hk) * sizeof(float) : 0);
     return w;
 }
+
+// acc[b][h][t] += sum of the softmax weights of token t over the G query
+// heads of kv head h, from the kept scores and the lse (tq_weights.cu).
+cudaError_t launch_weights(const ScoreArgs& m, const int32_t* seq_lens, const float* lse, float* acc,
+                           long long stride_b, long long stride_h, int Hk, int G, cudaStream_t st);
 
 // Whether rows acc + b * sb + h * sh of max_len elements do not overlap:
 // sequences of heads or heads of sequences (one writer per running sum).
@@ -150,11 +161,6 @@ inline bool acc_strides_ok(int B, int Hk, long long sb, long long sh, int max_le
     if (B <= 1 || Hk <= 1) return true;
     return sb >= (Hk - 1) * sh + max_len || sh >= (B - 1) * sb + max_len;
 }
-
-// acc[b][h][t] += sum of the softmax weights of token t over the G query
-// heads of kv head h, from the kept scores and the lse (tq_weights.cu).
-cudaError_t launch_weights(const ScoreArgs& m, const int32_t* seq_lens, const float* lse, float* acc,
-                           long long stride_b, long long stride_h, int B, int Hk, int G, cudaStream_t st);
 
 #ifdef __CUDACC__
 // The visible tokens of a sequence: [lo, pend) and [first, L), with
@@ -192,6 +198,105 @@ struct VisibleSet {
     __device__ __forceinline__ bool all(int t, int n) const
     {
         return (t >= lo && t + n <= pend) || (t >= first && t + n <= L);
+    }
+};
+// Which splits a batch of scored sequences has: all of `chunk` tiles (a
+// sequence's last one may be shorter), with the smallest chunk that gives at
+// most B * S of them, so that every CTA has the same work however the lengths,
+// windows and documents differ.  Split `id` of the launch belongs to sequence
+// b, as its split number id - base.  All threads of the block call this;
+// `area` is B + 4 ints of shared memory, free again afterwards.  The launch's
+// first block (`writer`) stores the plan for stage 2.  Batches above kPlanMax
+// sequences keep S splits for each.
+constexpr int kPlanMax = 512;
+struct SplitPlan {
+    int b, base, n, chunk;     // b < 0: no split of this number
+    __device__ SplitPlan(const ScoreArgs& m, const int32_t* seq_lens, int S, int id, bool writer, int* area)
+    {
+        auto tiles = [&](int i) {
+            const int len = seq_lens[i];
+            return len > m.max_len ? 1 : VisibleSet(m, len, i).tiles();      // too long: one split, which says so
+        };
+        if (m.B == 1 || m.B > kPlanMax) {
+            b = id / S;
+            const int t = tiles(b);
+            base = b * S;
+            chunk = max((t + S - 1) / S, 1);
+            n = (t + chunk - 1) / chunk;
+            if ((m.B == 1 ? writer : id == base) && threadIdx.x == 0) { m.plan[2 * b] = base; m.plan[2 * b + 1] = n; }
+            if (id - base >= n) b = -1;
+            return;
+        }
+        const int lane = threadIdx.x & 31;
+        if (m.B <= 32) {               // every warp for itself, a sequence per lane
+            const int t = lane < m.B ? tiles(lane) : 0;
+            chunk = chunk_of(t, t, S * m.B, m.B, [&](int c) { return (t + c - 1) / c; });
+            const int k = (t + chunk - 1) / chunk;
+            int incl = k;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            if (writer && threadIdx.x < m.B) { m.plan[2 * lane] = incl - k; m.plan[2 * lane + 1] = k; }
+            const unsigned here = __ballot_sync(0xffffffffu, id >= incl - k && id < incl);
+            b = here ? __ffs(here) - 1 : -1;
+            base = __shfl_sync(0xffffffffu, incl - k, max(b, 0));
+            n = __shfl_sync(0xffffffffu, k, max(b, 0));
+            return;
+        }
+        for (int i = threadIdx.x; i < m.B; i += blockDim.x) area[i] = tiles(i);
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const int B = m.B;
+            long long total = 0;
+            int most = 0;
+            for (int i = lane; i < B; i += 32) { total += area[i]; most = max(most, area[i]); }
+            const int c = chunk_of(total, most, S * B, B, [&](int c) {
+                int k = 0;
+                for (int i = lane; i < B; i += 32) k += (area[i] + c - 1) / c;
+                return k;
+            });
+            int run = 0;
+            if (lane == 0) area[B] = -1;
+            __syncwarp();
+            for (int i0 = 0; i0 < B; i0 += 32) {
+                const int i = i0 + lane, k = i < B ? (area[i] + c - 1) / c : 0;
+                int incl = k;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+                    if (lane >= d) incl += o;
+                }
+                const int first = run + incl - k;
+                if (id >= first && id < first + k) { area[B] = i; area[B + 1] = first; area[B + 2] = k; }
+                if (writer && i < B) { m.plan[2 * i] = first; m.plan[2 * i + 1] = k; }
+                run += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (lane == 0) area[B + 3] = c;
+        }
+        __syncthreads();
+        b = area[m.B];
+        base = area[m.B + 1];
+        n = area[m.B + 2];
+        chunk = area[m.B + 3];
+        __syncthreads();
+    }
+
+    // The smallest chunk with at most `slots` splits: a warp's search between
+    // the average share and what surely suffices.  total, most: each lane's
+    // share of the sequences' tiles and its longest; splits(c): its splits.
+    template <typename F>
+    static __device__ int chunk_of(long long total, int most, int slots, int B, F splits)
+    {
+        for (int k = 16; k; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
+        most = __reduce_max_sync(0xffffffffu, most);
+        int lo = int(max((total + slots - 1) / slots, 1LL));
+        int hi = max(slots > B ? int(min((total + slots - B - 1) / (slots - B), (long long)most)) : most, lo);
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            if (__reduce_add_sync(0xffffffffu, splits(mid)) <= slots) hi = mid;
+            else                                                      lo = mid + 1;
+        }
+        return lo;
     }
 };
 #endif

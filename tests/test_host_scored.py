@@ -53,7 +53,7 @@ def test_unsupported(bad):
 
 
 def test_workspace_too_small():
-    n = tq.tq_decode_workspace_bytes(2, 32, 1)
+    n = tq.tq_decode_scored_workspace_bytes(2, 32, 1)
     assert tq.tq_decode_attention_scored(*_decode_args(_mods(window=3), wsb=n - 1), None) == WS
     n = tq.tq_decode_weights_workspace_bytes(2, 32, 8, 1, 128, 64)
     assert tq.tq_decode_attention_weights(*_decode_args(None, wsb=n - 1), P, 8 * 64, 64, None) == WS
