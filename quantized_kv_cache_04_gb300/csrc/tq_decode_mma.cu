@@ -280,9 +280,11 @@ int launch_mma_stage1(const tq_layout& L, bool soa, int q_dtype, const void* que
     a.g = geom_of(L, soa);
     a.lpt = (B <= 512 && m.smem >= size_t(4) * (B + 1)) ? 1 : 0;
     a.mods = mods ? *mods : ScoreArgs{};
-    const cudaError_t e = mods                ? launch_mma_scored(a, q_dtype, B, m.smem, st)
-                          : v_threshold > 0.f ? launch_mma_sparse(a, q_dtype, B, m.smem, st)
-                                              : launch_mma_dense(a, q_dtype, B, m.smem, st);
+    a.mods.cap *= 1.4426950408889634f;               // the kernel's scores are in log2 units
+    a.mods.inv_cap *= 0.6931471805599453f;
+    const auto launch = mods ? (mods->scores ? launch_mma_weights : mods->cap > 0.f ? launch_mma_capped : launch_mma_scored)
+                        : v_threshold > 0.f ? launch_mma_sparse : launch_mma_dense;
+    const cudaError_t e = launch(a, q_dtype, B, m.smem, st);
     return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

@@ -80,18 +80,23 @@ struct MmaArgs {
     int stuck_tile;          // test hook: this tile of split 0, sequence 0, head group 0 is
                              // expected 16 bytes more than its copies bring (-1: none)
     SlotGeom g;
-    ScoreArgs mods;          // kScored instantiations only
+    ScoreArgs mods;          // kScored, kCapped and kWeights instantiations only
 };
 
 // What a stage-1 instantiation does beyond the plain decode: the sparse-V
-// gate, or the score modifiers (softcap, distance bias, visible tokens) with
-// the scores kept for the attention weights when asked.
-constexpr int kDense = 0, kSparse = 1, kScored = 2;
+// gate, or the score modifiers: distance bias and visible tokens (kScored),
+// softcap too (kCapped), and the scores kept for the attention weights as well
+// (kWeights, where a cap of 0 is none).  Modes, not branches: a branch between
+// the scores and the softmax ends the block in which the compiler overlaps a
+// tile's loads, lookups and MMAs.  The bias is always added (a slope of 0).
+constexpr int kDense = 0, kSparse = 1, kScored = 2, kCapped = 3, kWeights = 4;
 
 // Each mode is instantiated in its own translation unit.
 cudaError_t launch_mma_dense(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
 cudaError_t launch_mma_sparse(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
 cudaError_t launch_mma_scored(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
+cudaError_t launch_mma_capped(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
+cudaError_t launch_mma_weights(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
 
 namespace {
 
@@ -331,6 +336,20 @@ __device__ __forceinline__ int seq_of_rank(const int32_t* seq_lens, int B, int r
     const int b = sl[B];
     __syncthreads();                     // the area is reused afterwards
     return b;
+}
+
+// Stores of kept scores where `put`, without a branch and, as nothing in the
+// kernel reads them, without a memory clobber that would keep the compiler from
+// moving a tile's loads across.
+__device__ __forceinline__ void store_if(float* p, float x, int put)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %2, 0;\n\t@q st.global.f32 [%0], %1;\n\t}"
+                 ::"l"(p), "f"(x), "r"(put));
+}
+__device__ __forceinline__ void store_if(float* p, float x, float y, int put)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %3, 0;\n\t@q st.global.v2.f32 [%0], {%1, %2};\n\t}"
+                 ::"l"(p), "f"(x), "f"(y), "r"(put));
 }
 
 // Token order inside a 16-row tile: the MMAs' own.  QK row r is token r
@@ -635,11 +654,11 @@ __device__ __forceinline__ void pv_tile(const uint8_t* tile_v, int rs, int gid, 
 // G: 4 (columns = 4 heads x {hi, lo}) or 8 (columns = 8 heads).
 // One CTA = (split, sequence); warp w = kv head w; each iteration consumes a
 // 32-token tile (two 16-row MMA tiles) with one softmax update.
-// MODE: kDense, kSparse or kScored.
+// MODE: kDense, kSparse, kScored, kCapped or kWeights.
 template <typename TQ, int KMODE, int VBITS, int G, bool SOA, int MODE>
 __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__ MmaArgs a)
 {
-    constexpr bool SPARSE = MODE == kSparse, SCORED = MODE == kScored;
+    constexpr bool SPARSE = MODE == kSparse, SCORED = MODE >= kScored, CAPPED = MODE >= kCapped, KEEP = MODE == kWeights;
     extern __shared__ __align__(128) uint8_t smem[];
     // 3-bit keys: the code-pair centroid table (8 KB; one element elsewhere)
     __shared__ __align__(16) uint2 key_lut[KMODE == 3 ? kLut3Entries : KMODE == 4 ? kLut4Entries : 1];
@@ -692,13 +711,32 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     int t_begin = split * chunk;
     int t_end = min(L, t_begin + chunk);
     // scored: t_begin and t_end are positions in the list of tiles that hold
-    // visible tokens (32 per tile)
+    // visible tokens (32 per tile).  What the tile loop needs of the visible set
+    // lies in shared memory (registers are what G = 8 runs out of), as do the
+    // heads' slopes
     bool too_long = false;       // past what can be listed: a NaN lse, nothing read
-    [[maybe_unused]] VisibleSet vis(SCORED ? a.mods : ScoreArgs{}, SCORED ? min(L, a.mods.max_len) : 0, b);
+    __shared__ int s_vis[SCORED ? sizeof(VisibleSet) / 4 : 1];
+    __shared__ float s_slope[SCORED ? 16 * 8 : 1];
+    __shared__ float* s_keep[KEEP ? 16 : 1];      // where each warp's kv head keeps its scores
+    [[maybe_unused]] const VisibleSet& vis = *reinterpret_cast<const VisibleSet*>(s_vis);
+    __shared__ __align__(16) int s_tiles[SCORED ? 4 : 1];    // na, token of tile 0, of tile na less 32 na, last tile
     if constexpr (SCORED) {
-        t_end = min(vis.tiles() * kTile, t_begin + chunk);
+        const VisibleSet v(a.mods, min(L, a.mods.max_len), b);
+        t_end = min(v.tiles() * kTile, t_begin + chunk);
         too_long = L > a.mods.max_len;
+        if (threadIdx.x == 0) {
+            *reinterpret_cast<VisibleSet*>(s_vis) = v;
+            *reinterpret_cast<int4*>(s_tiles) = make_int4(v.na, v.base(0), (v.b0 - v.na) << 5, v.tiles() - 1);
+        }
+        if (KEEP && lane == 0)
+            s_keep[warp] = a.mods.scores + ((long long)b * a.Hk + h) * a.mods.vtok * a.mods.gp + qh0;
+        for (int i = threadIdx.x; i < Hc * 8; i += blockDim.x)
+            s_slope[i] = a.mods.slopes && i % 8 < Greal
+                             ? a.mods.slopes[(h0 + i / 8) * Gall + qh0 + i % 8] * 1.4426950408889634f : 0.f;
     }
+    // listed tile v: its first token, and whether it surely holds nothing hidden
+    auto vis_base = [&](int v) { return (v << 5) + (v < s_tiles[0] ? s_tiles[1] : s_tiles[2]); };
+    auto vis_whole = [&](int v) { return v != 0 && v + 1 != s_tiles[0] && v != s_tiles[0] && v != s_tiles[3]; };
 
     if (t_begin >= t_end || a.num_blocks <= 0 || (SCORED && too_long)) {
         // empty split: lse = -inf and a zero partial; tokens but no cache
@@ -724,6 +762,9 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int stage_bytes = kTile * (rs + mb);
     const int NST = a.nstages;
     const int ntiles = (t_end - t_begin + kTile - 1) / kTile;
+    // scored: the newest tokens first, whose biased scores are the largest, so
+    // that the running maximum seldom moves
+    auto vis_tile = [&](int tile) { return (t_begin >> 5) + ntiles - 1 - tile; };
     const int32_t* bt = a.block_table + (long long)b * a.bt_stride;
     const int lg = a.bs_log2;
     const int seg_rows = kTile < (1 << lg) ? kTile : (1 << lg);   // rows per page segment
@@ -777,7 +818,7 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         if (tile >= ntiles) return;
         uint8_t* dst = smem + stage * stage_bytes;
         uint64_t* bar = &full[stage];
-        const int tbase = SCORED ? vis.base((t_begin >> 5) + tile) : t_begin + tile * kTile;
+        const int tbase = SCORED ? vis_base(vis_tile(tile)) : t_begin + tile * kTile;
         // data rows: one copy per page segment when the CTA takes whole rows
         // and the shared stride equals the global one, or through the tensor
         // map (a box of the CTA's part of a segment's rows), else one per
@@ -787,13 +828,13 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         const bool seg_m = soa && mb == a.Hk * a.g.meta_bytes;
         const int len_d = seg_d ? seg_rows : 1, len_m = seg_m ? seg_rows : 1;   // rows per copy
         const int lg_d = seg_d ? seg_lg : 0, lg_m = seg_m ? seg_lg : 0;      // (powers of two)
-        const int nd = min(kTile >> lg_d, (L - tbase + len_d - 1) >> lg_d);
-        const int nm = soa ? min(kTile >> lg_m, (L - tbase + len_m - 1) >> lg_m) : 0;
+        const int nd = SCORED ? kTile >> lg_d : min(kTile >> lg_d, (L - tbase + len_d - 1) >> lg_d);
+        const int nm = !soa ? 0 : SCORED ? kTile >> lg_m : min(kTile >> lg_m, (L - tbase + len_m - 1) >> lg_m);
         // scored: only copies that bring a visible token (the pages of others
         // may have been freed)
         bool want_d = lane < nd, want_m = lane < nm;
         int cnt_d = nd, cnt_m = nm;
-        if constexpr (SCORED) {
+        if (SCORED && !vis_whole(vis_tile(tile))) {     // warp-uniform
             want_d = want_d && vis.any(tbase + lane * len_d, len_d);
             want_m = want_m && vis.any(tbase + lane * len_m, len_m);
             cnt_d = __popc(__ballot_sync(0xffffffffu, want_d));
@@ -999,23 +1040,6 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int mrs = soa ? mb : rs;
     const int moff = soa ? kTile * rs + warp * a.g.meta_bytes : hoff;
 
-    // scored: the cap and the head's slopes in log2 units, and this thread's
-    // score column (query heads qh0 + tig, or qh0 + 2 tig and the next)
-    [[maybe_unused]] float cap2 = 0.f, inv_cap2 = 0.f, slope2[NH] = {};
-    [[maybe_unused]] float* sc_out = nullptr;
-    if constexpr (SCORED) {
-        constexpr float kLog2e = 1.4426950408889634f;
-        cap2 = a.mods.cap * kLog2e;
-        inv_cap2 = a.mods.inv_cap * (1.f / kLog2e);
-#pragma unroll
-        for (int j = 0; j < NH; ++j) {
-            const int g = G == 4 ? tig : 2 * tig + j;
-            if (a.mods.slopes && g < Greal) slope2[j] = a.mods.slopes[h * Gall + qh0 + g] * kLog2e;
-        }
-        if (a.mods.scores)
-            sc_out = a.mods.scores + ((long long)b * a.Hk + h) * a.mods.vtok * a.mods.gp + qh0 + (G == 4 ? tig : 2 * tig);
-    }
-
     // One 32-token tile in stage memory st (this warp's slot at offset 0).
     // PARTIAL: some of its tokens lie at or past t_end and are masked.
     // KGEN: the general key path; false: 2-bit keys without the lo part
@@ -1074,27 +1098,27 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         }
 
         if constexpr (SCORED) {
-            // softcap, then the distance bias (distance: to the newest token)
-            if (a.mods.cap > 0.f) {
+            // softcap, then the distance bias (distance: to the newest token),
+            // in log2 units like the scores
+            if (CAPPED && (!KEEP || a.mods.cap > 0.f)) {
 #pragma unroll
                 for (int j = 0; j < NH; ++j) {
                     float x[4] = {s[j][0][0], s[j][0][1], s[j][1][0], s[j][1][1]};
-                    softcap_warp(x, cap2, inv_cap2);
+                    softcap_warp(x, a.mods.cap, a.mods.inv_cap);
                     s[j][0][0] = x[0];
                     s[j][0][1] = x[1];
                     s[j][1][0] = x[2];
                     s[j][1][1] = x[3];
                 }
             }
-            if (a.mods.slopes) {
+            const float dist0 = float(vis.L - 1 - t0 - tau0);
+#pragma unroll
+            for (int j = 0; j < NH; ++j) {
+                const float slope = s_slope[8 * warp + (G == 4 ? tig : 2 * tig + j)];
 #pragma unroll
                 for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float dist = float(L - 1 - (t0 + 16 * rt + (r ? tau1 : tau0)));
-#pragma unroll
-                        for (int j = 0; j < NH; ++j) s[j][rt][r] = fmaf(-slope2[j], dist, s[j][rt][r]);
-                    }
+                    for (int r = 0; r < 2; ++r) s[j][rt][r] = fmaf(-slope, dist0 - float(16 * rt + 8 * r), s[j][rt][r]);
             }
         }
 
@@ -1122,21 +1146,19 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             mt[j] = m;               // finite: the tile holds a valid token
             need |= m > m_run[j] + 8.f;
         }
-        if constexpr (SCORED) {
+        if constexpr (KEEP) {
             // the scores for the attention weights, masked tokens as -inf
-            if (a.mods.scores) {
+            float* p = s_keep[warp] + (unsigned long long)unsigned(vt + tau0) * unsigned(a.mods.gp) +
+                       (G == 4 ? tig : 2 * tig);
+            const int put = (G == 4 ? tig : 2 * tig) < Greal;
 #pragma unroll
-                for (int rt = 0; rt < 2; ++rt)
+            for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float* sp = sc_out + (long long)(vt + 16 * rt + (r ? tau1 : tau0)) * a.mods.gp;
-                        if constexpr (G == 4) {
-                            if (tig < Greal) *sp = s[0][rt][r];
-                        } else {
-                            if (2 * tig < Greal) *reinterpret_cast<float2*>(sp) = make_float2(s[0][rt][r], s[1][rt][r]);
-                        }
-                    }
-            }
+                for (int r = 0; r < 2; ++r) {
+                    if constexpr (G == 4) store_if(p, s[0][rt][r], put);
+                    else                  store_if(p, s[0][rt][r], s[1][rt][r], put);
+                    p += 8 * a.mods.gp;
+                }
         }
         need |= fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1])) > 128.f;
         if (__any_sync(0xffffffffu, need)) {
@@ -1209,9 +1231,9 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             if (!__all_sync(0xffffffffu, ok_wait)) return it;
             const uint8_t* st = smem + stage * stage_bytes + hoff;
             const uint8_t* sm = smem + stage * stage_bytes + moff;
-            const int vt = t_begin + it * kTile;
-            const int t0 = SCORED ? vis.base(vt >> 5) : vt;
-            const bool whole = SCORED ? vis.all(t0, kTile) : vt + kTile <= t_end;
+            const int vt = SCORED ? vis_tile(it) << 5 : t_begin + it * kTile;
+            const int t0 = SCORED ? vis_base(vt >> 5) : vt;
+            const bool whole = SCORED ? vis_whole(vt >> 5) : vt + kTile <= t_end;
             if (whole) tile(st, sm, t0, vt, std::false_type{}, lo_tag, km_tag, vm_tag);
             else       tile(st, sm, t0, vt, std::true_type{}, lo_tag, km_tag, vm_tag);
 

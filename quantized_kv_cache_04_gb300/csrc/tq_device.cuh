@@ -85,32 +85,39 @@ __device__ __forceinline__ void fwht128_half(float (&v)[8], int l)
     }
 }
 
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // cap * tanh(x / cap) for N scores of a thread (all lanes of the warp call).
-// |y| <= 1.5, y = x / cap: the sixth convergent of Lambert's continued fraction
-// tanh y = y / (1 + y^2 / (3 + y^2 / (5 + ...))), below 3.3e-8 of tanh y from it;
-// beyond, where tanh y >= 0.9: 1 - 2 / (1 + e^(2|y|)).  Both keep the error
-// relative to the value (a few fp32 steps), so small scores lose nothing.  The
-// second form is computed only when a lane of the warp needs it.
+// |y| <= 0.9, y = x / cap: the fifth convergent of Lambert's continued fraction
+// tanh y = y / (1 + y^2 / (3 + y^2 / (5 + ...))), within 2.3e-8 of tanh y, times
+// x in place of cap * y; beyond, where tanh y > 0.7: 1 - 2 / (1 + e^(2|y|)).  Both
+// keep the error relative to the value (a few fp32 steps), so small scores lose
+// nothing.  The second form is computed only when a lane of the warp needs it:
+// caps of 20 to 50 rarely bind.
 template <int N>
 __device__ __forceinline__ void softcap_warp(float (&x)[N], float cap, float inv_cap)
 {
-    float y[N], most = 0.f;
+    float c[N], most = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        y[i] = x[i] * inv_cap;
-        most = fmaxf(most, fabsf(y[i]));
-        const float z = y[i] * y[i];
-        const float num = fmaf(fmaf(21.f, z, 1260.f), z, 10395.f);
-        const float den = fmaf(fmaf(z + 210.f, z, 4725.f), z, 10395.f);
-        x[i] = cap * y[i] * __fdividef(num, den);
+        const float y = x[i] * inv_cap, z = y * y;
+        most = fmaxf(most, z);
+        c[i] = x[i] * (fmaf(z + 105.f, z, 945.f) * fast_rcp(fmaf(fmaf(15.f, z, 420.f), z, 945.f)));
     }
-    if (__any_sync(0xffffffffu, most > 1.5f)) {
+    if (__any_sync(0xffffffffu, most > 0.81f)) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float t = 1.f - __fdividef(2.f, 1.f + exp2f(fabsf(y[i]) * 2.8853900817779268f));
-            if (fabsf(y[i]) > 1.5f) x[i] = copysignf(cap * t, y[i]);
+            const float y = fabsf(x[i] * inv_cap);
+            if (y > 0.9f) c[i] = copysignf(cap * (1.f - 2.f * fast_rcp(1.f + exp2f(y * 2.8853900817779268f))), x[i]);
         }
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = c[i];
 }
 
 __device__ __forceinline__ uint16_t ld_u16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
