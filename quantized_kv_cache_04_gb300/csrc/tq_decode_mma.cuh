@@ -172,6 +172,19 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
 }
+// The same with the bytes first to leave the L2: cache rows of a call that
+// keeps its scores, so that the scores stay there for the weights kernel
+// (524K tokens, 64 query heads: 239 -> 234 us).
+__device__ __forceinline__ void bulk_g2s_once(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
 // One box of a 2-D tensor map (x: 32-bit words within a row, y: row) into
 // shared memory, completing on the mbarrier.  x * 4 is a multiple of 16.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar)
@@ -358,13 +371,6 @@ __device__ __forceinline__ void store_if(float* p, float x, float y, int put)
 // gid = 2 tig and 2 tig + 1).  With a shared row stride of 4 mod 8 words,
 // the key loads of a warp (8 rows, 12-16 bytes per lane) and its value loads
 // (4 rows 2 tig + c, 8 bytes per lane) touch distinct banks.
-
-__device__ __forceinline__ float fast_exp2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // two E4M3 pairs (low and high half of w) -> two f16x2
 __device__ __forceinline__ void cvt_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi)
@@ -864,7 +870,8 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             } else {
                 const uint8_t* src =
                     soa ? blk + off * drow + h0 * hs_g : blk + off * (long long)row_bytes + h0 * hs_g;
-                bulk_g2s(dst + lane * len_d * rs, src, uint32_t(len_d * cb), bar);
+                if constexpr (KEEP) bulk_g2s_once(dst + lane * len_d * rs, src, uint32_t(len_d * cb), bar);
+                else                bulk_g2s(dst + lane * len_d * rs, src, uint32_t(len_d * cb), bar);
             }
             if (soa && same) {
                 const uint8_t* meta = blk + (1LL << lg) * drow + ((long long)off * a.Hk + h0) * a.g.meta_bytes;

@@ -85,6 +85,13 @@ __device__ __forceinline__ void fwht128_half(float (&v)[8], int l)
     }
 }
 
+__device__ __forceinline__ float fast_exp2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float fast_rcp(float x)
 {
     float y;

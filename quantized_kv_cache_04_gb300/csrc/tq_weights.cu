@@ -16,14 +16,17 @@ namespace tq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 4;                  // tokens per thread, kThreads apart
 
-// GP: columns per listed token (0: m.gp).
+// tokens per thread, kThreads apart: as many as keep their scores in registers
+template <int GP> constexpr int kPerThread = GP > 8 ? 2 : 4;
+
+// GP: columns per listed token (m.gp).
 template <int GP>
 __global__ void __launch_bounds__(kThreads) weights_kernel(ScoreArgs m, const int32_t* seq_lens, const float* lse,
                                                            float* acc, long long stride_b, long long stride_h,
                                                            int Hk, int G)
 {
+    constexpr int kPer = kPerThread<GP>;
     __shared__ float s_lse[kMaxGroup];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int b = blockIdx.z, h = blockIdx.y;
@@ -34,9 +37,9 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(ScoreArgs m, const in
     if (v0 >= end) return;
     if (threadIdx.x < G)
         s_lse[threadIdx.x] = lse[((long long)b * Hk + h) * G + threadIdx.x] * 1.4426950408889634f;
-    const float* x = m.scores + ((long long)b * Hk + h) * m.vtok * m.gp;
+    const float* x = m.scores + ((long long)b * Hk + h) * m.vtok * GP;
     float* sums = acc + b * stride_b + h * stride_h;
-    float s[kPer][GP ? GP : 1], was[kPer];
+    float s[kPer][GP], was[kPer];
     int t[kPer];
     // every load of the thread's tokens before the arithmetic
 #pragma unroll
@@ -44,37 +47,55 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(ScoreArgs m, const in
         const int v = v0 + u * kThreads + threadIdx.x;
         t[u] = v < end ? vis.base(v >> 5) + (v & 31) : -1;
         if (t[u] >= 0 && !vis.sees(t[u])) t[u] = -1;
-        if (t[u] >= 0) was[u] = sums[t[u]];
-        if constexpr (GP > 0) {
-            if (t[u] >= 0) {
-                if constexpr (GP % 4 == 0) {
+        if (t[u] < 0) continue;
+        was[u] = sums[t[u]];
+        const float* xv = x + (unsigned long long)unsigned(v) * unsigned(GP);
+        if constexpr (GP % 4 == 0) {
 #pragma unroll
-                    for (int g = 0; g < GP; g += 4) {
-                        const float4 q = *reinterpret_cast<const float4*>(x + (long long)v * GP + g);
-                        s[u][g] = q.x; s[u][g + 1] = q.y; s[u][g + 2] = q.z; s[u][g + 3] = q.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int g = 0; g < GP; ++g) s[u][g] = x[(long long)v * GP + g];
-                }
+            for (int g = 0; g < GP; g += 4) {
+                const float4 q = __ldcs(reinterpret_cast<const float4*>(xv + g));
+                s[u][g] = q.x; s[u][g + 1] = q.y; s[u][g + 2] = q.z; s[u][g + 3] = q.w;
             }
+        } else if constexpr (GP % 2 == 0) {
+#pragma unroll
+            for (int g = 0; g < GP; g += 2) {
+                const float2 q = __ldcs(reinterpret_cast<const float2*>(xv + g));
+                s[u][g] = q.x; s[u][g + 1] = q.y;
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < GP; ++g) s[u][g] = __ldcs(xv + g);
         }
     }
     __syncthreads();
+    float l[GP];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) l[g] = s_lse[g];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-        if (t[u] < 0) continue;
         float w = 0.f;
-        if constexpr (GP > 0) {
 #pragma unroll
-            for (int g = 0; g < GP; ++g)
-                if (g < G) w += exp2f(s[u][g] - s_lse[g]);
-        } else {
-            const long long v = v0 + u * kThreads + threadIdx.x;
-            for (int g = 0; g < G; ++g) w += exp2f(x[v * m.gp + g] - s_lse[g]);
-        }
-        sums[t[u]] = was[u] + w;
+        for (int g = 0; g < GP; ++g)
+            if (g < G) w += fast_exp2(s[u][g] - l[g]);           // a padding column may hold anything
+        if (t[u] >= 0) sums[t[u]] = was[u] + w;
     }
+}
+
+template <int GP>
+cudaError_t launch_gp(const ScoreArgs& m, const int32_t* seq_lens, const float* lse, float* acc, long long stride_b,
+                      long long stride_h, int Hk, int G, cudaStream_t st)
+{
+    constexpr int kTokens = kThreads * kPerThread<GP>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((m.vtok + kTokens - 1) / kTokens, Hk, m.B);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, weights_kernel<GP>, m, seq_lens, lse, acc, stride_b, stride_h, Hk, G);
 }
 
 }  // namespace
@@ -83,20 +104,12 @@ cudaError_t launch_weights(const ScoreArgs& m, const int32_t* seq_lens, const fl
                            long long stride_b, long long stride_h, int Hk, int G, cudaStream_t st)
 {
     if (m.vtok == 0) return cudaSuccess;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((m.vtok + kThreads * kPer - 1) / (kThreads * kPer), Hk, m.B);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    // groups of up to 8 keep their tokens' scores in registers
-    auto k = m.gp == 8 ? weights_kernel<8> : m.gp == 6 ? weights_kernel<6> : m.gp == 4 ? weights_kernel<4>
-             : m.gp == 3 ? weights_kernel<3> : m.gp == 2 ? weights_kernel<2> : m.gp == 1 ? weights_kernel<1>
-                                                                                         : weights_kernel<0>;
-    return cudaLaunchKernelEx(&cfg, k, m, seq_lens, lse, acc, stride_b, stride_h, Hk, G);
+    switch (m.gp) {                          // score_heads(G), G <= 16
+#define TQ_GP(n) case n: return launch_gp<n>(m, seq_lens, lse, acc, stride_b, stride_h, Hk, G, st);
+    TQ_GP(1) TQ_GP(2) TQ_GP(3) TQ_GP(4) TQ_GP(6) TQ_GP(8) TQ_GP(10) TQ_GP(12) TQ_GP(14) TQ_GP(16)
+#undef TQ_GP
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace tq

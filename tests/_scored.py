@@ -76,9 +76,10 @@ def call(preset, q, d, Hk, bs, max_len, acc=None, num_splits=0, out_dtype=torch.
     out = torch.full((B, Hq, D), 7.0, dtype=out_dtype, device=dev)
     lse = torch.full((B, Hq), 7.0, device=dev) if want_lse else None
     if ws is None:
-        ws = torch.empty(tq.scored_workspace_bytes(preset, B, Hq, Hk, max_len, mods.get("window", 0),
-                                                   mods.get("prefix", 0), acc is not None, num_splits),
-                         dtype=torch.uint8, device=dev)
+        # whatever an earlier use left: NaN in every word
+        ws = torch.full((tq.scored_workspace_bytes(preset, B, Hq, Hk, max_len, mods.get("window", 0),
+                                                   mods.get("prefix", 0), acc is not None, num_splits),), 255,
+                        dtype=torch.uint8, device=dev)
     args = (preset, q, d["cache"], d["bt"], d["sl"], max_len, Hk, bs, d["signs"], d["cent"], out, lse, ws)
     if acc is None:
         tq.decode_attention_scored(*args, num_splits=num_splits, stream=stream, **mods)
