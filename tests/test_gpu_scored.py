@@ -299,3 +299,32 @@ def test_many_splits_and_long_context(orc):
             c.decode_weights(q.cuda(), bt, sl, n, out, lse, ws, acc, num_splits=S, **kw)
             check_decode(out.cpu().numpy(), lse.cpu().numpy(), o[None], l[None], f"{kw} S={S}")
             _check_acc(acc.cpu().numpy(), np.zeros((1, Hk, n), np.float32), [w], [n], G)
+
+
+@pytest.mark.parametrize("preset", [0, 2, 4])
+@pytest.mark.parametrize("G", [4, 8])
+def test_long_flat_softmax_keeps_fp32_accuracy(preset, G):
+    """Averages of 40000 values: the two parts of a value sum (codes times scales, and zeros) cancel to a few
+    thousandths of their size, and the output still has fp32 accuracy.  A score is off by up to 2^-20 of its size
+    (here < 8), so weights by 1e-5 at most and their average's error by a fraction of that; the sums round by
+    2^-24 per addition: 1e-5 of the output covers both, where sums that are not kept about the middle code
+    are some 1e-4 off."""
+    n, Hk, bs = 40000, 8, 64
+    gen = torch.Generator(device="cuda").manual_seed(preset)
+    nb = -(-n // bs)
+    c = tq.TQCache(preset, nb, bs, Hk)
+    t = torch.arange(n, device="cuda")
+    k, v = torch.empty((n, Hk, 128), device="cuda"), torch.empty((n, Hk, 128), device="cuda")
+    c.store(torch.randn((n, Hk, 128), generator=gen, device="cuda").half(),
+            torch.randn((n, Hk, 128), generator=gen, device="cuda").half(), t)
+    c.dequant(t, k, v)
+    q = torch.randn((1, Hk * G, 128), generator=gen, device="cuda").half()
+    x = torch.einsum("hgd,nhd->hgn", q.double().view(Hk, G, 128), k.double()) * 128 ** -0.5
+    w = torch.softmax(50.0 * torch.tanh(x / 50.0), -1)
+    want = torch.einsum("hgn,nhd->hgd", w, v.double()).reshape(1, Hk * G, 128)
+    out, lse = torch.empty((1, Hk * G, 128), device="cuda"), torch.empty((1, Hk * G), device="cuda")
+    bt = torch.arange(nb, dtype=torch.int32, device="cuda").view(1, -1)
+    sl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    for S in (0, 3):
+        c.decode_scored(q, bt, sl, n, out, lse, c.scored_workspace(1, Hk * G, n, S), num_splits=S, softcap=50.0)
+        assert ((out.double() - want).norm() / want.norm()).item() <= 1e-5
