@@ -318,7 +318,8 @@ int tq_decode_attention_noalloc(int preset, int head_dim, int batch, int num_q_h
  * first tokens (sinks) as masks of its decode; its other masks and the cap have
  * no counterpart on the pages.
  * alibi_slopes: device float[num_q_heads] or NULL; doc_start: device
- * int32[batch] or NULL; softcap >= 0 and finite, window >= 0, prefix >= 0. */
+ * int32[batch] or NULL; softcap 0 or from 1e-30 to 1e30, window >= 0,
+ * prefix >= 0. */
 typedef struct {
     float softcap;
     int window;
@@ -397,7 +398,7 @@ int tq_decode_attention_weights(int preset, int head_dim, int batch, int num_q_h
  * acc: device float, strides as there, read only.  keep: device
  * int32[batch][num_kv_heads][budget], the kept token indices ascending, -1
  * past a sequence of fewer tokens.  new_lens: device int32[batch], min(L,
- * budget).  A sequence longer than max_seq_len is a caller error: nothing of it
+ * budget); not seq_lens itself (TQ_ERR_INVALID_ARG).  A sequence longer than max_seq_len is a caller error: nothing of it
  * is read, its keep entries are -1 and its new_lens entry is L.
  * budget >= 1, prefix + recent <= budget, max_seq_len <= 2^30.  Returns TQ_OK, TQ_ERR_INVALID_ARG
  * or TQ_ERR_CUDA. */

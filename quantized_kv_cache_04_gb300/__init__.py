@@ -79,7 +79,7 @@ class TQCache:
         import torch
         nbytes = scored_workspace_bytes(self.preset, batch, num_q_heads, self.num_kv_heads, max_seq_len, window,
                                         prefix, weights, num_splits, self.head_dim)
-        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.cache.device)
 
     def decode_scored(self, query, block_table, seq_lens, max_seq_len, out, lse, workspace, num_splits=0,
                       softmax_scale=None, stream=None, **mods):
@@ -105,8 +105,8 @@ class TQCache:
             if stream is not None:
                 raise ValueError("evict: with a stream of the caller's, keep and new_lens are the caller's too")
             B = seq_lens.shape[0]
-            keep = torch.empty((B, self.num_kv_heads, int(budget)), dtype=torch.int32, device=self.device)
-            new_lens = torch.empty((B,), dtype=torch.int32, device=self.device)
+            keep = torch.empty((B, self.num_kv_heads, int(budget)), dtype=torch.int32, device=self.cache.device)
+            new_lens = torch.empty((B,), dtype=torch.int32, device=self.cache.device)
         evict_select(acc, seq_lens, max_seq_len, budget, keep, new_lens, prefix, recent, stream)
         evict_compact(self.preset, keep, seq_lens, self.cache, block_table, self.num_kv_heads, self.block_size,
                       acc, stream)

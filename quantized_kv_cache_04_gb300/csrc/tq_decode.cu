@@ -8,8 +8,10 @@
 // note (<Q H, H K> = <Q, K>, so q is rotated once and keys stay rotated).
 //
 // This file holds the host entry points, stage 2 (the log-sum-exp merge) and
-// the plain instantiations of the CUDA-core stage 1 (tq_decode_cores.cuh),
-// used for shapes the tensor-core stage 1 (tq_decode_mma.cu) does not serve.
+// the CUDA-core stage 1 used for shapes the tensor-core stage 1
+// (tq_decode_mma.cu) does not serve: one CTA per (split, kv head, sequence),
+// four warps striding over the split's tokens, 4 coordinates per lane, fp32
+// scores and online softmax, partials merged across warps in shared memory.
 #include "tq_decode_cores.cuh"
 
 #include <algorithm>
@@ -20,6 +22,156 @@
 namespace tq {
 
 namespace {
+
+template <typename TQ, bool KEY_FP8, int KBITS, int VBITS, int GM>
+__global__ void __launch_bounds__(kWarps * 32) stage1_kernel(DecodeArgs a)
+{
+    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.G, S = a.num_splits;
+    const int L = a.seq_lens[b];
+    const int chunk = (L + S - 1) / S;
+    const int t0 = split * chunk;
+    const int t1 = min(L, t0 + chunk);
+
+    __shared__ float s_cent[16];
+    __shared__ float s_m[kWarps][GM], s_l[kWarps][GM];
+    __shared__ float s_acc[kWarps][GM][kHeadDim];
+
+    if (t0 >= t1) {   // empty split: lse = -inf, zero partial output
+        for (int i = threadIdx.x; i < G * (kHeadDim + 1); i += blockDim.x) {
+            const int g = i / (kHeadDim + 1), d = i % (kHeadDim + 1);
+            float* m = a.mid + (((long long)b * a.Hq + h * G + g) * S + split) * (kHeadDim + 1);
+            m[d] = d == kHeadDim ? -INFINITY : 0.f;
+        }
+        return;
+    }
+    __shared__ int s_bad;        // a block-table entry outside [0, num_blocks) was met
+    if (threadIdx.x == 0) s_bad = 0;
+    if constexpr (!KEY_FP8) {
+        if (threadIdx.x < (1 << KBITS)) s_cent[threadIdx.x] = a.centroids[threadIdx.x];
+    }
+
+    // q (rotated once for MSE keys), pre-multiplied by the softmax scale
+    float qv[GM][4];
+    const TQ* Q = static_cast<const TQ*>(a.query);
+    float sgn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sgn[i] = KEY_FP8 ? 1.f : float(a.signs[4 * lane + i]);
+#pragma unroll
+    for (int g = 0; g < GM; ++g) {
+        if (g < G) {
+            const TQ* qp = Q + ((long long)b * a.Hq + h * G + g) * kHeadDim + 4 * lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qv[g][i] = sgn[i] * to_f32(qp[i]);
+            if constexpr (!KEY_FP8) {
+                fwht128_warp(qv[g], lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qv[g][i] *= 0.08838834764831845f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qv[g][i] *= a.scale;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qv[g][i] = 0.f;
+        }
+    }
+    __syncthreads();
+
+    float m[GM], l[GM], acc[GM][4];
+#pragma unroll
+    for (int g = 0; g < GM; ++g) {
+        m[g] = -INFINITY;
+        l[g] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[g][i] = 0.f;
+    }
+
+    const int32_t* bt = a.block_table + (long long)b * a.bt_stride;
+    const int lgbs = 31 - __clz(a.bs);       // block sizes are powers of two
+    bool bad = false;
+    for (int t = t0 + warp; t < t1; t += kWarps) {
+        const long long page = bt[t >> lgbs];
+        if (page < 0 || page >= a.num_blocks) { bad = true; continue; }   // not read; the rows become NaN
+        const uint8_t *sp, *mp;              // data and metadata of the record
+        slot_ptrs(a.g, a.cache, page, t & (a.bs - 1), h, a.bs, a.Hk, sp, mp);
+
+        float kv[4];
+        float knorm = 1.f;
+        if constexpr (KEY_FP8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                __half_raw hr = __nv_cvt_fp8_to_halfraw(sp[4 * lane + i], __NV_E4M3);
+                kv[i] = __half2float(__half(hr));
+            }
+        } else {
+            int c[4];
+            load_codes<KBITS>(sp, lane, c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kv[i] = s_cent[c[i]];
+            knorm = __half2float(__ushort_as_half(ld_u16(mp + a.g.m_norm)));
+        }
+        float s[GM];
+#pragma unroll
+        for (int g = 0; g < GM; ++g)
+            s[g] = warp_sum(qv[g][0] * kv[0] + qv[g][1] * kv[1] + qv[g][2] * kv[2] + qv[g][3] * kv[3]) * knorm;
+
+        // online softmax; sparse V: a row whose p is at most vthr keeps its
+        // weight in l but adds nothing to the value sum, and the value codes
+        // are not read when no head keeps the row (s is warp-uniform)
+        float al[GM], pv[GM];
+        bool anyv = false;
+#pragma unroll
+        for (int g = 0; g < GM; ++g) {
+            const float mn = fmaxf(m[g], s[g]);
+            const float p = expf(s[g] - mn);
+            al[g] = expf(m[g] - mn);
+            l[g] = l[g] * al[g] + p;
+            m[g] = mn;
+            pv[g] = p > a.vthr ? p : 0.f;
+            anyv |= g < G && pv[g] > 0.f;
+        }
+        float vv[4] = {0.f, 0.f, 0.f, 0.f};
+        if (anyv) {
+            int vc[4];
+            load_codes<VBITS>(sp + a.g.v_off, lane, vc);
+            const float vs = __half2float(__ushort_as_half(ld_u16(mp + a.g.m_scale)));
+            const float vz = __half2float(__ushort_as_half(ld_u16(mp + a.g.m_zero)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vv[i] = float(vc[i]) * vs + vz;
+        }
+#pragma unroll
+        for (int g = 0; g < GM; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[g][i] = acc[g][i] * al[g] + pv[g] * vv[i];
+    }
+
+    // merge the four warps' partials
+    if (bad && lane == 0) s_bad = 1;
+#pragma unroll
+    for (int g = 0; g < GM; ++g) {
+        if (lane == 0) { s_m[warp][g] = m[g]; s_l[warp][g] = l[g]; }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_acc[warp][g][4 * lane + i] = acc[g][i];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * kHeadDim; i += blockDim.x) {
+        const int g = i / kHeadDim, d = i % kHeadDim;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][g]);
+        float lsum = 0.f, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = s_m[w][g] == -INFINITY ? 0.f : expf(s_m[w][g] - M);
+            lsum += s_l[w][g] * f;
+            o += s_acc[w][g][d] * f;
+        }
+        float* mp = a.mid + (((long long)b * a.Hq + h * G + g) * S + split) * (kHeadDim + 1);
+        mp[d] = o / lsum;
+        if (d == 0) mp[kHeadDim] = s_bad ? __int_as_float(0x7fc00000) : M + logf(lsum);
+    }
+}
 
 // Stage 2: the log-sum-exp merge of the split partials.  A row (sequence,
 // query head) takes R = ceil(S / 16) warps (at most 8), each merging every
@@ -155,16 +307,41 @@ cudaError_t launch_stage2(const DecodeArgs& a, bool scored, cudaStream_t st)
     return scored ? launch_stage2<TO, true>(a, st) : launch_stage2<TO, false>(a, st);
 }
 
+template <typename TQ, bool FP8, int KB, int VB>
+cudaError_t launch_stage1_g(const DecodeArgs& a, cudaStream_t st)
+{
+    dim3 grid(a.num_splits, a.Hk, a.B);
+    if (a.G <= 1) stage1_kernel<TQ, FP8, KB, VB, 1><<<grid, kWarps * 32, 0, st>>>(a);
+    else if (a.G <= 2) stage1_kernel<TQ, FP8, KB, VB, 2><<<grid, kWarps * 32, 0, st>>>(a);
+    else if (a.G <= 4) stage1_kernel<TQ, FP8, KB, VB, 4><<<grid, kWarps * 32, 0, st>>>(a);
+    else if (a.G <= 8) stage1_kernel<TQ, FP8, KB, VB, 8><<<grid, kWarps * 32, 0, st>>>(a);
+    else stage1_kernel<TQ, FP8, KB, VB, 16><<<grid, kWarps * 32, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename TQ>
+cudaError_t launch_stage1(int preset, const DecodeArgs& a, cudaStream_t st)
+{
+    switch (preset & 0xFF) {
+    case TQ_K8V4:    return launch_stage1_g<TQ, true, 4, 4>(a, st);
+    case TQ_4BIT_NC: return launch_stage1_g<TQ, false, 4, 4>(a, st);
+    case TQ_K3V4_NC: return launch_stage1_g<TQ, false, 3, 4>(a, st);
+    case TQ_3BIT_NC: return launch_stage1_g<TQ, false, 3, 3>(a, st);
+    case TQ_2BIT_NC: return launch_stage1_g<TQ, false, 2, 2>(a, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
 template <bool FP8, int KB, int VB>
 int v1_slots(int G, int num_sms)
 {
     int per_sm = 0;
     cudaError_t e;
-    if (G <= 1) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 1, false>, kWarps * 32, 0);
-    else if (G <= 2) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 2, false>, kWarps * 32, 0);
-    else if (G <= 4) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 4, false>, kWarps * 32, 0);
-    else if (G <= 8) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 8, false>, kWarps * 32, 0);
-    else e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 16, false>, kWarps * 32, 0);
+    if (G <= 1) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 1>, kWarps * 32, 0);
+    else if (G <= 2) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 2>, kWarps * 32, 0);
+    else if (G <= 4) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 4>, kWarps * 32, 0);
+    else if (G <= 8) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 8>, kWarps * 32, 0);
+    else e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stage1_kernel<__nv_bfloat16, FP8, KB, VB, 16>, kWarps * 32, 0);
     return e == cudaSuccess ? per_sm * num_sms : 0;
 }
 
@@ -247,10 +424,11 @@ int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int nu
 namespace tq {
 namespace {
 
-// Host-side checks of score modifiers (device arrays are not read).
+// Host-side checks of score modifiers (device arrays are not read).  Between
+// the bounds a cap and its reciprocal are finite, in log2 units too.
 bool mods_ok(const tq_score_mods& m)
 {
-    return m.softcap >= 0.f && m.softcap <= 3.0e38f && m.window >= 0 && m.prefix >= 0;
+    return (m.softcap == 0.f || (m.softcap >= 1e-30f && m.softcap <= 1e30f)) && m.window >= 0 && m.prefix >= 0;
 }
 
 // Split count of a scored decode, for the longest visible length.  Down to one
@@ -361,8 +539,8 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
     } else if (mods) {
         if (launch_cores_scored(preset, q_dtype, a, st) != cudaSuccess) return TQ_ERR_CUDA;
     } else {
-        cudaError_t e = q_dtype == TQ_F16 ? launch_stage1<__half, false>(preset, a, st)
-                                          : launch_stage1<__nv_bfloat16, false>(preset, a, st);
+        cudaError_t e = q_dtype == TQ_F16 ? launch_stage1<__half>(preset, a, st)
+                                          : launch_stage1<__nv_bfloat16>(preset, a, st);
         if (e != cudaSuccess) return TQ_ERR_CUDA;
     }
     const cudaError_t e2 = out_dtype == TQ_F32   ? launch_stage2<float>(a, mods != nullptr, st)

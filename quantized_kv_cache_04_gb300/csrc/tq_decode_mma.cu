@@ -12,8 +12,8 @@ namespace tq {
 
 cudaError_t launch_mma_dense(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st)
 {
-    return q_dtype == TQ_F16 ? launch_q<__half, kDense>(a, B, smem, st)
-                             : launch_q<__nv_bfloat16, kDense>(a, B, smem, st);
+    return q_dtype == TQ_F16 ? launch_q<__half, false>(a, B, smem, st)
+                             : launch_q<__nv_bfloat16, false>(a, B, smem, st);
 }
 
 namespace {
@@ -155,8 +155,8 @@ MmaGeom mma_geom(const tq_layout& L, bool soa, int Hk, int G)
 template <int KMODE, int VBITS, int G>
 int slots_t(const MmaGeom& m, bool soa, int num_sms)
 {
-    auto k = soa ? stage1_mma_kernel<__nv_bfloat16, KMODE, VBITS, G, true, kDense>
-                 : stage1_mma_kernel<__nv_bfloat16, KMODE, VBITS, G, false, kDense>;
+    auto k = soa ? stage1_mma_kernel<__nv_bfloat16, KMODE, VBITS, G, true, false>
+                 : stage1_mma_kernel<__nv_bfloat16, KMODE, VBITS, G, false, false>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(m.smem)) != cudaSuccess)
         return 0;
     int per_sm = 0;

@@ -80,20 +80,15 @@ struct MmaArgs {
     int stuck_tile;          // test hook: this tile of split 0, sequence 0, head group 0 is
                              // expected 16 bytes more than its copies bring (-1: none)
     SlotGeom g;
-    ScoreArgs mods;          // kScored, kCapped and kWeights instantiations only
+    ScoreArgs mods;          // scored kernel only (tq_decode_mma_scored.cuh)
 };
 
-// What a stage-1 instantiation does beyond the plain decode: the sparse-V
-// gate, or the score modifiers: distance bias and visible tokens (kScored),
-// softcap too (kCapped), and the scores kept for the attention weights as well
-// (kWeights, where a cap of 0 is none).  Modes, not branches: a branch between
-// the scores and the softmax ends the block in which the compiler overlaps a
-// tile's loads, lookups and MMAs.  The bias is always added (a slope of 0).
-constexpr int kDense = 0, kSparse = 1, kScored = 2, kCapped = 3, kWeights = 4;
-
-// Each mode is instantiated in its own translation unit.
+// Stage 1 with the value sum of every row (dense) or with the sparse-V gate;
+// each is instantiated in its own translation unit.
 cudaError_t launch_mma_dense(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
 cudaError_t launch_mma_sparse(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
+
+// The scored kernel's launchers (tq_decode_mma_scored.cuh).
 cudaError_t launch_mma_scored(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
 cudaError_t launch_mma_capped(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
 cudaError_t launch_mma_weights(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st);
@@ -170,19 +165,6 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
             smem_u32(dst)),
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
-// The same with the bytes first to leave the L2: cache rows of a call that
-// keeps its scores, so that the scores stay there for the weights kernel
-// (524K tokens, 64 query heads: 239 -> 234 us).
-__device__ __forceinline__ void bulk_g2s_once(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
-{
-    uint64_t policy;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 // One box of a 2-D tensor map (x: 32-bit words within a row, y: row) into
@@ -349,20 +331,6 @@ __device__ __forceinline__ int seq_of_rank(const int32_t* seq_lens, int B, int r
     const int b = sl[B];
     __syncthreads();                     // the area is reused afterwards
     return b;
-}
-
-// Stores of kept scores where `put`, without a branch and, as nothing in the
-// kernel reads them, without a memory clobber that would keep the compiler from
-// moving a tile's loads across.
-__device__ __forceinline__ void store_if(float* p, float x, int put)
-{
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %2, 0;\n\t@q st.global.f32 [%0], %1;\n\t}"
-                 ::"l"(p), "f"(x), "r"(put));
-}
-__device__ __forceinline__ void store_if(float* p, float x, float y, int put)
-{
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %3, 0;\n\t@q st.global.v2.f32 [%0], {%1, %2};\n\t}"
-                 ::"l"(p), "f"(x), "f"(y), "r"(put));
 }
 
 // Token order inside a 16-row tile: the MMAs' own.  QK row r is token r
@@ -660,11 +628,9 @@ __device__ __forceinline__ void pv_tile(const uint8_t* tile_v, int rs, int gid, 
 // G: 4 (columns = 4 heads x {hi, lo}) or 8 (columns = 8 heads).
 // One CTA = (split, sequence); warp w = kv head w; each iteration consumes a
 // 32-token tile (two 16-row MMA tiles) with one softmax update.
-// MODE: kDense, kSparse, kScored, kCapped or kWeights.
-template <typename TQ, int KMODE, int VBITS, int G, bool SOA, int MODE>
+template <typename TQ, int KMODE, int VBITS, int G, bool SOA, bool SPARSE>
 __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__ MmaArgs a)
 {
-    constexpr bool SPARSE = MODE == kSparse, SCORED = MODE >= kScored, CAPPED = MODE >= kCapped, KEEP = MODE == kWeights;
     extern __shared__ __align__(128) uint8_t smem[];
     // 3-bit keys: the code-pair centroid table (8 KB; one element elsewhere)
     __shared__ __align__(16) uint2 key_lut[KMODE == 3 ? kLut3Entries : KMODE == 4 ? kLut4Entries : 1];
@@ -679,20 +645,9 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int ngroups = a.Hk / a.hpc;
     const int kvg = blockIdx.x % ngroups;     // which hpc kv heads
     const int qg = (blockIdx.x / ngroups) % a.nqg;   // which 8 query heads of each kv head (G > 8)
-    int split = blockIdx.x / ngroups / a.nqg, b, chunk;
-    // scored: the launch's splits go by the plan of the batch (SplitPlan)
-    [[maybe_unused]] int id = 0;
-    if constexpr (SCORED) {
-        id = blockIdx.y * a.num_splits + split;
-        const SplitPlan plan(a.mods, a.seq_lens, a.num_splits, id, blockIdx.x == 0 && blockIdx.y == 0,
-                             reinterpret_cast<int*>(smem));
-        if (plan.b < 0) return;
-        b = plan.b;
-        split = id - plan.base;
-        chunk = plan.chunk * kTile;
-    } else {
-        b = a.lpt ? seq_of_rank(a.seq_lens, gridDim.y, blockIdx.y, reinterpret_cast<int*>(smem)) : blockIdx.y;
-    }
+    const int split = blockIdx.x / ngroups / a.nqg;
+    const int b = a.lpt ? seq_of_rank(a.seq_lens, gridDim.y, blockIdx.y, reinterpret_cast<int*>(smem))
+                        : blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3;
     const int h0 = kvg * a.hpc;               // first kv head of this CTA
@@ -706,52 +661,20 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int nwarps = blockDim.x >> 5;
 
     const int L = a.seq_lens[b];
-    if constexpr (!SCORED) {
-        chunk = (L + S - 1) / S;
-        chunk = (chunk + kTile - 1) / kTile * kTile;
-    }
-    // this split's partial of query head hq
-    auto partial = [&](int hq) {
-        return a.mid + (SCORED ? (long long)id * Hq + hq : ((long long)b * Hq + hq) * S + split) * (kHeadDim + 1);
-    };
-    int t_begin = split * chunk;
-    int t_end = min(L, t_begin + chunk);
-    // scored: t_begin and t_end are positions in the list of tiles that hold
-    // visible tokens (32 per tile).  What the tile loop needs of the visible set
-    // lies in shared memory (registers are what G = 8 runs out of), as do the
-    // heads' slopes
-    bool too_long = false;       // past what can be listed: a NaN lse, nothing read
-    __shared__ int s_vis[SCORED ? sizeof(VisibleSet) / 4 : 1];
-    __shared__ float s_slope[SCORED ? 16 * 8 : 1];
-    __shared__ float* s_keep[KEEP ? 16 : 1];      // where each warp's kv head keeps its scores
-    [[maybe_unused]] const VisibleSet& vis = *reinterpret_cast<const VisibleSet*>(s_vis);
-    __shared__ __align__(16) int s_tiles[SCORED ? 4 : 1];    // na, token of tile 0, of tile na less 32 na, last tile
-    if constexpr (SCORED) {
-        const VisibleSet v(a.mods, min(L, a.mods.max_len), b);
-        t_end = min(v.tiles() * kTile, t_begin + chunk);
-        too_long = L > a.mods.max_len;
-        if (threadIdx.x == 0) {
-            *reinterpret_cast<VisibleSet*>(s_vis) = v;
-            *reinterpret_cast<int4*>(s_tiles) = make_int4(v.na, v.base(0), (v.b0 - v.na) << 5, v.tiles() - 1);
-        }
-        if (KEEP && lane == 0)
-            s_keep[warp] = a.mods.scores + ((long long)b * a.Hk + h) * a.mods.vtok * a.mods.gp + qh0;
-        for (int i = threadIdx.x; i < Hc * 8; i += blockDim.x)
-            s_slope[i] = a.mods.slopes && i % 8 < Greal
-                             ? a.mods.slopes[(h0 + i / 8) * Gall + qh0 + i % 8] * 1.4426950408889634f : 0.f;
-    }
-    // listed tile v: its first token, and whether it surely holds nothing hidden
-    auto vis_base = [&](int v) { return (v << 5) + (v < s_tiles[0] ? s_tiles[1] : s_tiles[2]); };
-    auto vis_whole = [&](int v) { return v != 0 && v + 1 != s_tiles[0] && v != s_tiles[0] && v != s_tiles[3]; };
+    int chunk = (L + S - 1) / S;
+    chunk = (chunk + kTile - 1) / kTile * kTile;
+    const int t_begin = split * chunk;
+    const int t_end = min(L, t_begin + chunk);
 
-    if (t_begin >= t_end || a.num_blocks <= 0 || (SCORED && too_long)) {
+    if (t_begin >= t_end || a.num_blocks <= 0) {
         // empty split: lse = -inf and a zero partial; tokens but no cache
         // block to read them from: a NaN lse
-        const float lse0 = t_begin >= t_end && !too_long ? -INFINITY : __int_as_float(0x7fc00000);
+        const float lse0 = t_begin >= t_end ? -INFINITY : __int_as_float(0x7fc00000);
         for (int i = threadIdx.x; i < Hc * Greal * (kHeadDim + 1); i += blockDim.x) {
             const int r = i / (kHeadDim + 1), d = i % (kHeadDim + 1);
             const int hq = (h0 + r / Greal) * Gall + qh0 + r % Greal;
-            partial(hq)[d] = d == kHeadDim ? lse0 : 0.f;
+            float* m = a.mid + (((long long)b * Hq + hq) * S + split) * (kHeadDim + 1);
+            m[d] = d == kHeadDim ? lse0 : 0.f;
         }
         return;
     }
@@ -768,9 +691,6 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     const int stage_bytes = kTile * (rs + mb);
     const int NST = a.nstages;
     const int ntiles = (t_end - t_begin + kTile - 1) / kTile;
-    // scored: the newest tokens first, whose biased scores are the largest, so
-    // that the running maximum seldom moves
-    auto vis_tile = [&](int tile) { return (t_begin >> 5) + ntiles - 1 - tile; };
     const int32_t* bt = a.block_table + (long long)b * a.bt_stride;
     const int lg = a.bs_log2;
     const int seg_rows = kTile < (1 << lg) ? kTile : (1 << lg);   // rows per page segment
@@ -824,7 +744,7 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         if (tile >= ntiles) return;
         uint8_t* dst = smem + stage * stage_bytes;
         uint64_t* bar = &full[stage];
-        const int tbase = SCORED ? vis_base(vis_tile(tile)) : t_begin + tile * kTile;
+        const int tbase = t_begin + tile * kTile;
         // data rows: one copy per page segment when the CTA takes whole rows
         // and the shared stride equals the global one, or through the tensor
         // map (a box of the CTA's part of a segment's rows), else one per
@@ -834,32 +754,22 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         const bool seg_m = soa && mb == a.Hk * a.g.meta_bytes;
         const int len_d = seg_d ? seg_rows : 1, len_m = seg_m ? seg_rows : 1;   // rows per copy
         const int lg_d = seg_d ? seg_lg : 0, lg_m = seg_m ? seg_lg : 0;      // (powers of two)
-        const int nd = SCORED ? kTile >> lg_d : min(kTile >> lg_d, (L - tbase + len_d - 1) >> lg_d);
-        const int nm = !soa ? 0 : SCORED ? kTile >> lg_m : min(kTile >> lg_m, (L - tbase + len_m - 1) >> lg_m);
-        // scored: only copies that bring a visible token (the pages of others
-        // may have been freed)
-        bool want_d = lane < nd, want_m = lane < nm;
-        int cnt_d = nd, cnt_m = nm;
-        if (SCORED && !vis_whole(vis_tile(tile))) {     // warp-uniform
-            want_d = want_d && vis.any(tbase + lane * len_d, len_d);
-            want_m = want_m && vis.any(tbase + lane * len_m, len_m);
-            cnt_d = __popc(__ballot_sync(0xffffffffu, want_d));
-            if constexpr (soa) cnt_m = __popc(__ballot_sync(0xffffffffu, want_m));
-        }
+        const int nd = min(kTile >> lg_d, (L - tbase + len_d - 1) >> lg_d);
+        const int nm = soa ? min(kTile >> lg_m, (L - tbase + len_m - 1) >> lg_m) : 0;
         if (lane == 0) {
             fence_async_shared();             // prior generic reads of this stage before the async writes
             // the test hook's tile expects 16 bytes that no copy brings: its
             // stage never completes and the bounded waits run out
             const uint32_t extra =
                 (tile == a.stuck_tile && split == 0 && qg == 0 && b == 0 && kvg == 0) ? 16u : 0u;
-            mbar_expect_tx(bar, uint32_t(cnt_d * len_d * cb + cnt_m * len_m * mb) + extra);
+            mbar_expect_tx(bar, uint32_t(nd * len_d * cb + nm * len_m * mb) + extra);
         }
         __syncwarp();
         const bool same = !soa || len_d == len_m;     // one address computation for both copies
         // a block-table entry outside [0, num_blocks) is replaced by page 0,
         // so nothing outside the cache is read, and noted: the CTA's rows
         // come out NaN (see the end of the kernel)
-        if (want_d) {
+        if (lane < nd) {
             const int t = tbase + lane * len_d;
             long long page = bt[t >> lg];
             if ((unsigned long long)page >= (unsigned long long)a.num_blocks) { page = 0; bad_seen = true; }
@@ -870,15 +780,14 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             } else {
                 const uint8_t* src =
                     soa ? blk + off * drow + h0 * hs_g : blk + off * (long long)row_bytes + h0 * hs_g;
-                if constexpr (KEEP) bulk_g2s_once(dst + lane * len_d * rs, src, uint32_t(len_d * cb), bar);
-                else                bulk_g2s(dst + lane * len_d * rs, src, uint32_t(len_d * cb), bar);
+                bulk_g2s(dst + lane * len_d * rs, src, uint32_t(len_d * cb), bar);
             }
             if (soa && same) {
                 const uint8_t* meta = blk + (1LL << lg) * drow + ((long long)off * a.Hk + h0) * a.g.meta_bytes;
                 bulk_g2s(dst + kTile * rs + lane * len_m * mb, meta, uint32_t(len_m * mb), bar);
             }
         }
-        if (!same && want_m) {
+        if (!same && lane < nm) {
             const int t = tbase + lane * len_m;
             long long page = bt[t >> lg];
             if ((unsigned long long)page >= (unsigned long long)a.num_blocks) { page = 0; bad_seen = true; }
@@ -1037,7 +946,6 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
-    constexpr float kMidCode = 0.5f * float((1 << VBITS) - 1);
     const int tau0 = gid, tau1 = gid + 8;      // this thread's QK rows
     const uint32_t l8 = uint32_t(lane & 15) * 8;   // this lane's copy in a pair-table entry
     const int hoff = warp * int(hs_g);         // this warp's slot (SoA: data record) in a shared row
@@ -1053,9 +961,8 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     // KGEN: the general key path; false: 2-bit keys without the lo part
     // (key_alpha)
     // KM / VM: the key / value misalignment of this warp's slot (0 or 2)
-    // vt: scored, the tile's first position in the list of visible tiles
-    auto tile = [&](const uint8_t* st, const uint8_t* sm, int t0, [[maybe_unused]] int vt, auto partial_tag,
-                    auto lo_tag, auto km_tag, auto vm_tag) {
+    auto tile = [&](const uint8_t* st, const uint8_t* sm, int t0, auto partial_tag, auto lo_tag,
+                    auto km_tag, auto vm_tag) {
         constexpr bool PARTIAL = decltype(partial_tag)::value;
         [[maybe_unused]] constexpr bool KGEN = decltype(lo_tag)::value;
         constexpr int KM = decltype(km_tag)::value, VM = decltype(vm_tag)::value;
@@ -1087,17 +994,8 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             vz[rt][0] = lds_f16(m0 + a.g.m_zero);
             vs[rt][1] = lds_f16(m1 + a.g.m_scale);
             vz[rt][1] = lds_f16(m1 + a.g.m_zero);
-            if constexpr (SCORED) {
-                vz[rt][0] = fmaf(kMidCode, vs[rt][0], vz[rt][0]);
-                vz[rt][1] = fmaf(kMidCode, vs[rt][1], vz[rt][1]);
-            }
-            if constexpr (SCORED) {
-                ok[rt][0] = !PARTIAL || vis.sees(t0 + 16 * rt + tau0);
-                ok[rt][1] = !PARTIAL || vis.sees(t0 + 16 * rt + tau1);
-            } else {
-                ok[rt][0] = !PARTIAL || t0 + 16 * rt + tau0 < t_end;
-                ok[rt][1] = !PARTIAL || t0 + 16 * rt + tau1 < t_end;
-            }
+            ok[rt][0] = !PARTIAL || t0 + 16 * rt + tau0 < t_end;
+            ok[rt][1] = !PARTIAL || t0 + 16 * rt + tau1 < t_end;
             if constexpr (G == 4) {
                 s[0][rt][0] = (sc[0] + sc[1]) * n0;
                 s[0][rt][1] = (sc[2] + sc[3]) * n1;
@@ -1106,31 +1004,6 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
                 s[1][rt][0] = (sc[1] + scl[1]) * n0;
                 s[0][rt][1] = (sc[2] + scl[2]) * n1;
                 s[1][rt][1] = (sc[3] + scl[3]) * n1;
-            }
-        }
-
-        if constexpr (SCORED) {
-            // softcap, then the distance bias (distance: to the newest token),
-            // in log2 units like the scores
-            if (CAPPED && (!KEEP || a.mods.cap > 0.f)) {
-#pragma unroll
-                for (int j = 0; j < NH; ++j) {
-                    float x[4] = {s[j][0][0], s[j][0][1], s[j][1][0], s[j][1][1]};
-                    softcap_warp(x, a.mods.cap, a.mods.inv_cap);
-                    s[j][0][0] = x[0];
-                    s[j][0][1] = x[1];
-                    s[j][1][0] = x[2];
-                    s[j][1][1] = x[3];
-                }
-            }
-            const float dist0 = float(vis.L - 1 - t0 - tau0);
-#pragma unroll
-            for (int j = 0; j < NH; ++j) {
-                const float slope = s_slope[8 * warp + (G == 4 ? tig : 2 * tig + j)];
-#pragma unroll
-                for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) s[j][rt][r] = fmaf(-slope, dist0 - float(16 * rt + 8 * r), s[j][rt][r]);
             }
         }
 
@@ -1155,22 +1028,8 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            mt[j] = m;               // finite: the tile holds a valid token
+            mt[j] = m;               // finite: the tile's first token is valid
             need |= m > m_run[j] + 8.f;
-        }
-        if constexpr (KEEP) {
-            // the scores for the attention weights, masked tokens as -inf
-            float* p = s_keep[warp] + (unsigned long long)unsigned(vt + tau0) * unsigned(a.mods.gp) +
-                       (G == 4 ? tig : 2 * tig);
-            const int put = (G == 4 ? tig : 2 * tig) < Greal;
-#pragma unroll
-            for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    if constexpr (G == 4) store_if(p, s[0][rt][r], put);
-                    else                  store_if(p, s[0][rt][r], s[1][rt][r], put);
-                    p += 8 * a.mods.gp;
-                }
         }
         need |= fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1])) > 128.f;
         if (__any_sync(0xffffffffu, need)) {
@@ -1219,23 +1078,6 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
                 }
             l_run[j] += lsum;
             z_run[j] += zsum;
-            // Scored: the value sum is kept about the middle code, sum p scale
-            // (code - mid) + sum p (zero + mid scale): over long contexts its two
-            // parts, sum p scale code and sum p zero, nearly cancel, and the MMAs'
-            // accumulation rounds towards zero.  So the accumulators give up mid
-            // times the tile's sum of P' (without it the output is 3.5e-4 off,
-            // relatively, at 131072 tokens and groups of 8).
-            if constexpr (SCORED) {
-                float d = (pp[0][j][0] + pp[0][j][1]) + (pp[1][j][0] + pp[1][j][1]);
-#pragma unroll
-                for (int m = 4; m < 32; m <<= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
-                d *= kMidCode / 512.f;         // the accumulators hold 2^-9 of the sums
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[i][j] -= d;            // G = 4: column 2 tig, the head's hi part
-                    acc[i][j + 2] -= d;
-                }
-            }
         }
 
         // ---- values
@@ -1260,11 +1102,9 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             if (!__all_sync(0xffffffffu, ok_wait)) return it;
             const uint8_t* st = smem + stage * stage_bytes + hoff;
             const uint8_t* sm = smem + stage * stage_bytes + moff;
-            const int vt = SCORED ? vis_tile(it) << 5 : t_begin + it * kTile;
-            const int t0 = SCORED ? vis_base(vt >> 5) : vt;
-            const bool whole = SCORED ? vis_whole(vt >> 5) : vt + kTile <= t_end;
-            if (whole) tile(st, sm, t0, vt, std::false_type{}, lo_tag, km_tag, vm_tag);
-            else       tile(st, sm, t0, vt, std::true_type{}, lo_tag, km_tag, vm_tag);
+            const int t0 = t_begin + it * kTile;
+            if (t0 + kTile <= t_end) tile(st, sm, t0, std::false_type{}, lo_tag, km_tag, vm_tag);
+            else                     tile(st, sm, t0, std::true_type{}, lo_tag, km_tag, vm_tag);
 
             // ---- this warp is done with the stage; the last warp refills it
             __syncwarp();
@@ -1321,7 +1161,8 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         __syncwarp();
         if (last && *reinterpret_cast<volatile int*>(bad_pages))
             for (int i = lane; i < Hc * Greal; i += 32)
-                partial((h0 + i / Greal) * Gall + qh0 + i % Greal)[kHeadDim] = __int_as_float(0x7fc00000);
+                a.mid[(((long long)b * Hq + (h0 + i / Greal) * Gall + qh0 + i % Greal) * S + split) *
+                          (kHeadDim + 1) + kHeadDim] = __int_as_float(0x7fc00000);
     };
     if (failed_at >= 0) {
         // let the copies that may still be in flight (tiles failed_at ..
@@ -1330,7 +1171,8 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
         for (int it = failed_at; it < min(ntiles, failed_at + NST); ++it)
             mbar_wait(&full[it % NST], uint32_t((it / NST) & 1), a.wait_polls);
         if (lane < Greal)
-            partial(h * Gall + qh0 + lane)[kHeadDim] = __int_as_float(0x7fc00000);
+            a.mid[(((long long)b * Hq + h * Gall + qh0 + lane) * S + split) * (kHeadDim + 1) + kHeadDim] =
+                __int_as_float(0x7fc00000);
         finish();
     } else {
         // ---------------- epilogue: finish the row sums, write o_s and lse_s.
@@ -1348,7 +1190,7 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
             const int g = G == 4 ? tig : 2 * tig + j;
             if (g >= Greal) continue;
             const int hq = h * Gall + qh0 + g;
-            float* mp = partial(hq);
+            float* mp = a.mid + (((long long)b * Hq + hq) * S + split) * (kHeadDim + 1);
             const float inv = 1.f / l_run[j];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -1375,11 +1217,11 @@ __global__ void __launch_bounds__(512) stage1_mma_kernel(const __grid_constant__
     }
 }
 
-template <typename TQ, int KMODE, int VBITS, int G, int MODE>
+template <typename TQ, int KMODE, int VBITS, int G, bool SPARSE>
 cudaError_t launch_t(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
 {
-    auto k = a.g.soa ? stage1_mma_kernel<TQ, KMODE, VBITS, G, true, MODE>
-                     : stage1_mma_kernel<TQ, KMODE, VBITS, G, false, MODE>;
+    auto k = a.g.soa ? stage1_mma_kernel<TQ, KMODE, VBITS, G, true, SPARSE>
+                     : stage1_mma_kernel<TQ, KMODE, VBITS, G, false, SPARSE>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1395,21 +1237,21 @@ cudaError_t launch_t(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-template <typename TQ, int KMODE, int VBITS, int MODE>
+template <typename TQ, int KMODE, int VBITS, bool SPARSE>
 cudaError_t launch_g(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
 {
-    return a.G <= 4 ? launch_t<TQ, KMODE, VBITS, 4, MODE>(a, B, smem, st)
-                    : launch_t<TQ, KMODE, VBITS, 8, MODE>(a, B, smem, st);
+    return a.G <= 4 ? launch_t<TQ, KMODE, VBITS, 4, SPARSE>(a, B, smem, st)
+                    : launch_t<TQ, KMODE, VBITS, 8, SPARSE>(a, B, smem, st);
 }
 
-template <typename TQ, int MODE>
+template <typename TQ, bool SPARSE>
 cudaError_t launch_q(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
 {
-    if (a.g.key_fp8) return launch_g<TQ, 8, 4, MODE>(a, B, smem, st);
-    if (a.g.key_bits == 4) return launch_g<TQ, 4, 4, MODE>(a, B, smem, st);
-    if (a.g.key_bits == 2) return launch_g<TQ, 2, 2, MODE>(a, B, smem, st);
-    if (a.g.value_bits == 4) return launch_g<TQ, 3, 4, MODE>(a, B, smem, st);
-    return launch_g<TQ, 3, 3, MODE>(a, B, smem, st);
+    if (a.g.key_fp8) return launch_g<TQ, 8, 4, SPARSE>(a, B, smem, st);
+    if (a.g.key_bits == 4) return launch_g<TQ, 4, 4, SPARSE>(a, B, smem, st);
+    if (a.g.key_bits == 2) return launch_g<TQ, 2, 2, SPARSE>(a, B, smem, st);
+    if (a.g.value_bits == 4) return launch_g<TQ, 3, 4, SPARSE>(a, B, smem, st);
+    return launch_g<TQ, 3, 3, SPARSE>(a, B, smem, st);
 }
 
 }  // namespace

@@ -6,8 +6,8 @@ namespace tq {
 
 cudaError_t launch_mma_sparse(const MmaArgs& a, int q_dtype, int B, size_t smem, cudaStream_t st)
 {
-    return q_dtype == TQ_F16 ? launch_q<__half, kSparse>(a, B, smem, st)
-                             : launch_q<__nv_bfloat16, kSparse>(a, B, smem, st);
+    return q_dtype == TQ_F16 ? launch_q<__half, true>(a, B, smem, st)
+                             : launch_q<__nv_bfloat16, true>(a, B, smem, st);
 }
 
 }  // namespace tq

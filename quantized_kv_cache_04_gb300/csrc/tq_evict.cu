@@ -604,6 +604,8 @@ extern "C" int tq_evict_select(int batch, int num_kv_heads, const float* acc, lo
         return TQ_ERR_INVALID_ARG;
     if (batch == 0) return TQ_OK;
     if (!acc || !seq_lens || !keep || !new_lens) return TQ_ERR_INVALID_ARG;
+    // every row reads the old lengths while the new ones are written
+    if (new_lens < seq_lens + batch && seq_lens < new_lens + batch) return TQ_ERR_INVALID_ARG;
     SelectArgs a;
     a.acc = acc;
     a.stride_b = acc_stride_seq;

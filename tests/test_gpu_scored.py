@@ -301,14 +301,58 @@ def test_many_splits_and_long_context(orc):
             _check_acc(acc.cpu().numpy(), np.zeros((1, Hk, n), np.float32), [w], [n], G)
 
 
+@pytest.mark.parametrize("preset,Hk", [(2, 8), (0, 2), (2, 1)])
+@pytest.mark.parametrize("B", [33, 40, 512, 520])
+def test_large_ragged_batches(preset, Hk, B):
+    """The plan of the splits for batches of more sequences than a warp has lanes, and than it plans for: every
+    row equals the same sequence decoded alone, within the decode's bars."""
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    rng = np.random.default_rng(B)
+    G, bs = 4, 16
+    lens = rng.integers(0, 200, B)
+    lens[:4] = [700, 0, 1, 200]
+    need = -(-lens // bs)
+    c = tq.TQCache(preset, int(need.sum()) + 1, bs, Hk)
+    bt = torch.full((B, int(need.max())), int(need.sum()), dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        bt[b, :n] = torch.arange(at, at + int(n), device="cuda")
+        at += int(n)
+    slots = torch.arange(int(need.sum()) * bs, device="cuda")
+    kv = torch.randn((2, slots.numel(), Hk, 128), generator=gen, device="cuda").half()
+    c.store(kv[0], kv[1], slots)
+    q = torch.randn((B, Hk * G, 128), generator=gen, device="cuda").half()
+    sl = torch.from_numpy(lens.astype(np.int32)).cuda()
+    d = dict(cache=c.cache, bt=bt, sl=sl, signs=c.signs, cent=c.centroids)
+    kw = dict(softcap=20.0, window=150, prefix=5)
+    for S in (0, 1, 3):
+        acc = torch.zeros((B, Hk, 704), device="cuda")
+        out, lse = call(preset, q, d, Hk, bs, 700, acc=acc, num_splits=S, **kw)
+        for b in (0, 1, 2, 3, B // 2, B - 1):
+            one = dict(d, bt=bt[b:b + 1], sl=sl[b:b + 1])
+            acc1 = torch.zeros((1, Hk, 704), device="cuda")
+            o1, l1 = call(preset, q[b:b + 1].contiguous(), one, Hk, bs, 700, acc=acc1, num_splits=1, **kw)
+            assert (out[b] - o1[0]).abs().max() <= 2e-5
+            assert torch.equal(lse[b].isneginf(), l1[0].isneginf())
+            assert (lse[b] - l1[0]).nan_to_num(0.0).abs().max() <= LSE_ABS
+            assert ((acc[b] - acc1[0]).abs() <= 2 * LSE_ABS * acc1[0]).all()
+        # every sequence with tokens weighs G in all
+        total = acc.double().sum(-1)
+        assert (total[sl > 0] - G).abs().max() <= G * 2 * LSE_ABS and (total[sl == 0] == 0).all()
+
+
 @pytest.mark.parametrize("preset", [0, 2, 4])
 @pytest.mark.parametrize("G", [4, 8])
 def test_long_flat_softmax_keeps_fp32_accuracy(preset, G):
     """Averages of 40000 values: the two parts of a value sum (codes times scales, and zeros) cancel to a few
-    thousandths of their size, and the output still has fp32 accuracy.  A score is off by up to 2^-20 of its size
-    (here < 8), so weights by 1e-5 at most and their average's error by a fraction of that; the sums round by
-    2^-24 per addition: 1e-5 of the output covers both, where sums that are not kept about the middle code
-    are some 1e-4 off."""
+    thousandths of their size, and the error must not grow with the sum.
+
+    The bound.  Per 32-token tile the accumulators give up m = (half the values' range) * (the tile's weight), then
+    at most four MMAs add terms that come back to it; each rounds towards zero, by at most 2^-23 of an
+    intermediate no larger than m.  Over all tiles: 4 * 2^-23 = 2^-21 of the weighted mean of half the range, per
+    output element.  Scores (of size < 8) are off by up to 2^-20 of their size, weights by 8e-6, independently
+    from token to token, their average by less than 1e-5 of itself.  (Sums that are not kept about the middle code
+    round by 2^-23 of everything summed so far, some hundred tiles: a factor of ten and more above the bound.)"""
     n, Hk, bs = 40000, 8, 64
     gen = torch.Generator(device="cuda").manual_seed(preset)
     nb = -(-n // bs)
@@ -327,4 +371,7 @@ def test_long_flat_softmax_keeps_fp32_accuracy(preset, G):
     sl = torch.tensor([n], dtype=torch.int32, device="cuda")
     for S in (0, 3):
         c.decode_scored(q, bt, sl, n, out, lse, c.scored_workspace(1, Hk * G, n, S), num_splits=S, softcap=50.0)
-        assert ((out.double() - want).norm() / want.norm()).item() <= 1e-5
+        half = ((v.amax(-1) - v.amin(-1)) / 2).double()                  # (n, Hk)
+        half = (w * half.t()[:, None]).sum(-1).max()
+        bound = 2.0 ** -21 * half * want.numel() ** 0.5 + 1e-5 * want.norm()
+        assert ((out.double() - want).norm() <= bound).item()

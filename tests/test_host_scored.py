@@ -39,7 +39,7 @@ def test_arguments_out_of_range(bad):
     assert tq.tq_decode_attention_weights(*_decode_args(m, **BAD[bad]), P, 8 * 64, 64, None) == INV
 
 
-@pytest.mark.parametrize("bad", [dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")),
+@pytest.mark.parametrize("bad", [dict(softcap=-1.0), dict(softcap=1e-31), dict(softcap=2e30), dict(softcap=float("nan")), dict(softcap=float("inf")),
                                  dict(window=-1), dict(prefix=-1), dict(window=4, prefix=-2)])
 def test_modifiers_out_of_range(bad):
     assert tq.tq_decode_attention_scored(*_decode_args(_mods(**bad)), None) == INV
@@ -69,7 +69,7 @@ def test_sums_that_overlap(acc, sb, sh):
 
 
 def _select(**kw):
-    a = dict(B=2, Hk=8, acc=P, sb=512, sh=64, sl=P, maxlen=64, budget=16, prefix=4, recent=4, keep=P, new=P)
+    a = dict(B=2, Hk=8, acc=P, sb=512, sh=64, sl=P, maxlen=64, budget=16, prefix=4, recent=4, keep=P, new=2 * P)
     a.update(kw)
     return tq.tq_evict_select(*a.values(), None)
 
@@ -83,7 +83,7 @@ def _compact(**kw):
 
 @pytest.mark.parametrize("bad", [dict(B=-1), dict(Hk=0), dict(budget=0), dict(prefix=-1), dict(recent=-1),
                                  dict(prefix=10, recent=7), dict(prefix=2 ** 31 - 1, recent=2 ** 31 - 1),
-                                 dict(maxlen=-1), dict(maxlen=2 ** 30 + 1, sb=2 ** 40, sh=2 ** 31), dict(sl=0), dict(keep=0), dict(new=0)])
+                                 dict(maxlen=-1), dict(maxlen=2 ** 30 + 1, sb=2 ** 40, sh=2 ** 31), dict(sl=0), dict(keep=0), dict(new=0), dict(new=P), dict(new=P + 4), dict(new=P - 4)])
 def test_select_arguments(bad):
     assert _select(**bad) == INV
 
