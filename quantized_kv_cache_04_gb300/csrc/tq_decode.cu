@@ -347,9 +347,9 @@ int v1_slots(int G, int num_sms)
 
 // (CTAs per split, resident CTA slots) of the stage-1 kernel for a shape,
 // cached per device.
-void stage1_shape(const tq_layout& L, bool soa, int Hk, int G, int* cps, int* slots)
+void stage1_shape(const tq_layout& L, bool soa, int Hk, int G, bool scored, int* cps, int* slots)
 {
-    struct Entry { int dev, kf8, kb, vb, soa, hk, g, cps, slots; };
+    struct Entry { int dev, kf8, kb, vb, soa, hk, g, scored, cps, slots; };
     static std::mutex mu;
     static std::vector<Entry> cache;
     int dev = -1, num_sms = 0;
@@ -363,14 +363,14 @@ void stage1_shape(const tq_layout& L, bool soa, int Hk, int G, int* cps, int* sl
         std::lock_guard<std::mutex> lock(mu);
         for (const Entry& e : cache)
             if (e.dev == dev && e.kf8 == L.key_fp8 && e.kb == L.key_bits && e.vb == L.value_bits &&
-                e.soa == int(soa) && e.hk == Hk && e.g == G) {
+                e.soa == int(soa) && e.hk == Hk && e.g == G && e.scored == int(scored)) {
                 *cps = e.cps;
                 *slots = e.slots;
                 return;
             }
     }
     int c = Hk, n = 0;
-    if (mma_stage1_supported(L, soa, Hk, G)) {
+    if (scored ? mma_scored_supported(L, soa, Hk, G) : mma_stage1_supported(L, soa, Hk, G)) {
         mma_stage1_shape(L, soa, Hk, G, num_sms, &c, &n);
     } else if (num_sms > 0) {
         c = Hk;                    // grid (splits, kv heads, batch)
@@ -385,7 +385,7 @@ void stage1_shape(const tq_layout& L, bool soa, int Hk, int G, int* cps, int* sl
         n = 2 * kNumSMs;           // no device to ask: two CTAs per SM of a GB300
     }
     std::lock_guard<std::mutex> lock(mu);
-    if (cache.size() < 256) cache.push_back({dev, L.key_fp8, L.key_bits, L.value_bits, int(soa), Hk, G, c, n});
+    if (cache.size() < 256) cache.push_back({dev, L.key_fp8, L.key_bits, L.value_bits, int(soa), Hk, G, int(scored), c, n});
     *cps = c;
     *slots = n;
 }
@@ -393,11 +393,11 @@ void stage1_shape(const tq_layout& L, bool soa, int Hk, int G, int* cps, int* sl
 }  // namespace
 
 int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int num_kv_heads, int max_seq_len,
-                int min_split)
+                int min_split, bool scored)
 {
     if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || max_seq_len <= 0) return 1;
     int cps = 1, slots = 1;
-    stage1_shape(L, soa, num_kv_heads, num_q_heads / num_kv_heads, &cps, &slots);
+    stage1_shape(L, soa, num_kv_heads, num_q_heads / num_kv_heads, scored, &cps, &slots);
     // Critical path of stage 1 in 32-token tiles: the CTAs of all splits run
     // in ceil(CTAs / slots) waves, each as long as one split's tiles plus a
     // fixed start-up (q preparation, first copy latency, epilogue) worth about
@@ -437,7 +437,7 @@ bool mods_ok(const tq_score_mods& m)
 // with 16 splits, 20.5 with 32, 18.5 with 64).
 int pick_scored_splits(const tq_layout& L, bool soa, int batch, int Hq, int Hk, int max_len, int window, int prefix)
 {
-    return pick_splits(L, soa, batch, Hq, Hk, std::min(max_len, 32 * visible_tiles(max_len, window, prefix)), 32);
+    return pick_splits(L, soa, batch, Hq, Hk, std::min(max_len, 32 * visible_tiles(max_len, window, prefix)), 32, true);
 }
 
 // Where a call that accumulates attention weights adds them.
@@ -528,7 +528,8 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
 
-    const bool mma = mma_stage1_supported(L, soa, num_kv_heads, a.G);
+    const bool mma = mods ? mma_scored_supported(L, soa, num_kv_heads, a.G)
+                          : mma_stage1_supported(L, soa, num_kv_heads, a.G);
     if (stuck_tile >= 0 && !mma) return TQ_ERR_UNSUPPORTED;
     if (mma) {
         rc = launch_mma_stage1(L, soa, q_dtype, query, kv_cache, num_blocks, block_table, block_table_stride, seq_lens,

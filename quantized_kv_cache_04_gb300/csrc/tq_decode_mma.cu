@@ -204,6 +204,23 @@ bool mma_stage1_supported(const tq_layout& L, bool soa, int num_kv_heads, int gr
            2 * kTile * (row + 16 + m.meta_bytes) <= 110 * 1024;
 }
 
+// The scored kernel also takes what the plain one leaves to the CUDA cores for
+// its alignment alone.  Where a CTA takes every kv head, both regions of a page
+// segment (16 or 32 tokens) are whole 16-byte units and lie at multiples of 16
+// bytes whatever a token's part of them is: SoA metadata of any size, and AoS
+// rows of 2 mod 4 bytes (kHalfRows).
+bool mma_scored_supported(const tq_layout& L, bool soa, int num_kv_heads, int group)
+{
+    if (mma_stage1_supported(L, soa, num_kv_heads, group)) return true;
+    const bool keys_ok = L.key_fp8 ? L.value_bits == 4
+                                   : L.key_bits == 3 || (L.key_bits == 4 && L.value_bits == 4) ||
+                                         (L.key_bits == 2 && L.value_bits == 2);
+    if (!keys_ok || num_kv_heads < 1 || group < 1 || group > kMaxGroup) return false;
+    const MmaGeom m = mma_geom(L, soa, num_kv_heads, group);
+    const bool rows_ok = soa ? m.copy_bytes % 16 == 0 : m.smem_row == m.copy_bytes && m.copy_bytes % 2 == 0;
+    return m.hpc == num_kv_heads && m.hpc <= 16 && rows_ok && 2 * kTile * (m.copy_bytes + 16 + m.meta_bytes) <= 110 * 1024;
+}
+
 void mma_stage1_shape(const tq_layout& L, bool soa, int num_kv_heads, int group, int num_sms,
                       int* ctas_per_split, int* slots)
 {

@@ -231,10 +231,21 @@ __device__ __forceinline__ void tmem_wait_ld()
 // n little-endian 32-bit words starting at the 2-byte aligned shared address p.
 // `mis` (0 or 2, uniform per warp) is p mod 4.  MIS = 0 or 2 fixes it at
 // compile time (the tile loop is instantiated per warp misalignment: a
-// branch in the loop costs more than the loads); MIS = -1 reads `mis`.
+// branch in the loop costs more than the loads); MIS = -1 reads `mis`;
+// MIS = -2 goes by each lane's address (token rows of 2 mod 4 bytes).
 template <int N, int MIS = -1>
 __device__ __forceinline__ void lds_words(const uint8_t* p, int mis, uint32_t (&w)[N])
 {
+    if constexpr (MIS == -2) {
+        const uint32_t m = smem_u32(p) & 2u;
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p - m);
+        uint32_t r[N + 1];
+#pragma unroll
+        for (int i = 0; i <= N; ++i) r[i] = q[i];
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(r[i], r[i + 1], 8 * m);
+        return;
+    }
     if (MIS == 0 || (MIS < 0 && mis == 0)) {
         const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
 #pragma unroll
@@ -568,7 +579,7 @@ __device__ __forceinline__ void pv_tile(const uint8_t* tile_v, int rs, int gid, 
             // 3 bits: dims 16 gid .. 16 gid + 15 are the 48 bits from byte
             // 6 gid, inside the two aligned words from 6 gid - m (m = its
             // misalignment, 0 or 2); spread to two nibble words
-            const int m = ((VM >= 0 ? VM : vmis) + 2 * (gid & 1)) & 2;
+            const int m = VM == -2 ? int(smem_u32(rv + 6 * gid) & 2u) : ((VM >= 0 ? VM : vmis) + 2 * (gid & 1)) & 2;
             const uint32_t* q = reinterpret_cast<const uint32_t*>(rv + 6 * gid - m);
             const uint32_t x0 = q[0], x1 = q[1];
             const uint32_t lo = __funnelshift_r(x0, x1, 8 * m), hi = x1 >> (8 * m);

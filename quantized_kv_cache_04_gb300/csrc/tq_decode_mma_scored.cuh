@@ -27,6 +27,7 @@ namespace tq {
 namespace {
 
 constexpr int kScored = 0, kCapped = 1, kWeights = 2;
+constexpr int kWordRows = 0, kSoa = 1, kHalfRows = 2;
 
 // The same with the bytes first to leave the L2: cache rows of a call that
 // keeps its scores, so that the scores stay there for the weights kernel
@@ -55,10 +56,13 @@ __device__ __forceinline__ void store_if(float* p, float x, float y, int put)
                  ::"l"(p), "f"(x), "f"(y), "r"(put));
 }
 
-template <typename TQ, int KMODE, int VBITS, int G, bool SOA, int MODE>
+// LAY: kWordRows (AoS, token rows of whole 32-bit words), kSoa, or kHalfRows (AoS
+// rows of 2 mod 4 bytes, e.g. 3 kv heads of 118-byte slots: every load finds its
+// own misalignment).
+template <typename TQ, int KMODE, int VBITS, int G, int LAY, int MODE>
 __global__ void __launch_bounds__(512) scored_mma_kernel(const __grid_constant__ MmaArgs a)
 {
-    constexpr bool CAPPED = MODE != kScored, KEEP = MODE == kWeights;
+    constexpr bool CAPPED = MODE != kScored, KEEP = MODE == kWeights, SOA = LAY == kSoa;
     extern __shared__ __align__(128) uint8_t smem[];
     // 3-bit keys: the code-pair centroid table (8 KB; one element elsewhere)
     __shared__ __align__(16) uint2 key_lut[KMODE == 3 ? kLut3Entries : KMODE == 4 ? kLut4Entries : 1];
@@ -636,7 +640,10 @@ __global__ void __launch_bounds__(512) scored_mma_kernel(const __grid_constant__
     using M2 = std::integral_constant<int, 2>;
     using MR = std::integral_constant<int, -1>;
     auto run_mis = [&](auto lo_tag) {
-        if constexpr (KMODE == 8) return run(lo_tag, M0{}, M0{});
+        if constexpr (LAY == kHalfRows) {
+            using ML = std::integral_constant<int, -2>;
+            return run(lo_tag, ML{}, ML{});
+        } else if constexpr (KMODE == 8) return run(lo_tag, M0{}, M0{});
         else if constexpr (KMODE == 3 && VBITS == 3) {
             if (kmis == 0) return vmis == 0 ? run(lo_tag, M0{}, M0{}) : run(lo_tag, M0{}, M2{});
             else           return vmis == 0 ? run(lo_tag, M2{}, M0{}) : run(lo_tag, M2{}, M2{});
@@ -722,8 +729,10 @@ __global__ void __launch_bounds__(512) scored_mma_kernel(const __grid_constant__
 template <typename TQ, int KMODE, int VBITS, int G, int MODE>
 cudaError_t launch_scored_t(const MmaArgs& a, int B, size_t smem, cudaStream_t st)
 {
-    auto k = a.g.soa ? scored_mma_kernel<TQ, KMODE, VBITS, G, true, MODE>
-                     : scored_mma_kernel<TQ, KMODE, VBITS, G, false, MODE>;
+    auto k = a.g.soa ? scored_mma_kernel<TQ, KMODE, VBITS, G, kSoa, MODE>
+                     : scored_mma_kernel<TQ, KMODE, VBITS, G, kWordRows, MODE>;
+    if constexpr (KMODE != 8)                // FP8-key slots are whole words
+        if (!a.g.soa && a.row_bytes % 4) k = scored_mma_kernel<TQ, KMODE, VBITS, G, kHalfRows, MODE>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

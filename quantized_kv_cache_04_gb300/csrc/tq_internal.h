@@ -17,7 +17,7 @@ int fill_layout(int preset, int head_dim, tq_layout* L);
 // Split count for num_splits = 0 (tq_decode.cu): the one that minimises the
 // stage-1 critical path over the resident CTA slots of the kernel that runs.
 int pick_splits(const tq_layout& L, bool soa, int batch, int num_q_heads, int num_kv_heads, int max_seq_len,
-                int min_split = 128);
+                int min_split = 128, bool scored = false);
 
 inline bool block_size_ok(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 inline bool in_dtype_ok(int dt) { return dt == TQ_F16 || dt == TQ_BF16; }
@@ -303,6 +303,7 @@ struct SplitPlan {
 
 // Tensor-core stage 1 (tq_decode_mma.cu): which shapes it serves, and its launcher.
 bool mma_stage1_supported(const tq_layout& L, bool soa, int num_kv_heads, int group);
+bool mma_scored_supported(const tq_layout& L, bool soa, int num_kv_heads, int group);   // its scored kernel
 // CTAs one split of one sequence launches, and resident CTA slots on num_sms
 // SMs (0 when the occupancy query fails, e.g. without a device).
 void mma_stage1_shape(const tq_layout& L, bool soa, int num_kv_heads, int group, int num_sms,

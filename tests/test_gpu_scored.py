@@ -28,8 +28,13 @@ SHAPES = {
     "g16": (16, 4, 32, [190, 31], 2),
     "g5": (5, 4, 128, [140, 96], 0),
     "g1": (1, 8, 32, [222, 17], 5),
-    "cores": (3, 3, 16, [211, 45, 0], 4),
-    "cores1": (4, 1, 32, [130, 64], 2),
+    # rows of 2 mod 4 bytes (Lloyd-Max presets), SoA metadata of 6 and 18 bytes a token
+    "odd3": (3, 3, 16, [211, 45, 0], 4),
+    "odd1": (4, 1, 32, [130, 64], 2),
+    "odd5": (8, 5, 16, [100, 37], 2),
+    # rows above what the tensor-core kernels take (CUDA cores, but for 2-bit slots and FP8 keys)
+    "wide": (2, 16, 16, [75, 40], 2),
+    "wide17": (9, 17, 32, [50, 33], 2),
 }
 MODS = {
     "cap": dict(softcap=5.0),
