@@ -422,7 +422,9 @@ int tq_evict_select(int batch, int num_kv_heads, const float* acc, long long acc
  * slots.  Pages must belong to one sequence each (a shared page would be moved
  * under the other's feet): copy them first.
  * Layouts (AoS and TQ_LAYOUT_SOA), block sizes and head_dim as tq_store;
- * max_seq_len <= 2^30. */
+ * num_kv_heads <= 4096, max_seq_len <= 2^30.  The table must hold
+ * ceil(seq_lens[b]/block_size) entries per row of up to max_seq_len tokens (not
+ * checked). */
 int tq_evict_compact(int preset, int head_dim, int batch, int num_kv_heads, int block_size,
                      uint8_t* kv_cache, long long num_blocks, const int32_t* block_table,
                      int block_table_stride, const int32_t* keep, int budget,

@@ -207,7 +207,8 @@ struct VisibleSet {
 // b, as its split number id - base.  All threads of the block call this;
 // `area` is B + 4 ints of shared memory, free again afterwards.  The launch's
 // first block (`writer`) stores the plan for stage 2.  Batches above kPlanMax
-// sequences keep S splits for each.
+// sequences keep S splits for each.  (Four sequences of packed documents, 3-bit
+// keys, 282K visible tokens in all: 209 us with S splits for each, 143 us so.)
 constexpr int kPlanMax = 512;
 struct SplitPlan {
     int b, base, n, chunk;     // b < 0: no split of this number

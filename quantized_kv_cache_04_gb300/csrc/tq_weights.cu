@@ -7,7 +7,9 @@
 //   acc[b][h][t] += sum_g 2^(x[g][t] - lse[g] log2 e)
 // over the G query heads of kv head h.  Each running sum has one writer and a
 // fixed order of additions.  Bound by bytes: 4 G per token of scores, which come
-// from L2 where they fit it, and 8 of sums.
+// from L2 where they fit it, and 8 of sums.  Measured: 524K tokens, 8 kv heads,
+// groups of 8 (134 MB of scores): 27 us, 5.7 TB/s at the DRAM; with one token per
+// thread at a time 36 us.
 #include "tq.h"
 #include "tq_device.cuh"
 #include "tq_internal.h"
