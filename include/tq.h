@@ -344,7 +344,8 @@ size_t tq_decode_scored_workspace_bytes(int batch, int num_q_heads, int num_spli
  * tiles that hold visible tokens: batch * num_splits splits of one size, given
  * out to the sequences by their visible lengths (batches above 512 sequences:
  * num_splits for each).
- * workspace: >= tq_decode_scored_workspace_bytes for the split count used.
+ * workspace: >= tq_decode_scored_workspace_bytes for the split count used
+ * (TQ_ERR_WORKSPACE); calls that overlap on the GPU need one each.
  * Other arguments, results, errors and supported shapes as
  * tq_decode_attention; TQ_ERR_INVALID_ARG for modifiers out of range or
  * max_seq_len above 2^30. */

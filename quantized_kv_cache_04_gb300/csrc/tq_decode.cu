@@ -465,7 +465,8 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
         return TQ_ERR_UNSUPPORTED;
     if (batch < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads ||
         num_blocks < 0 || block_table_stride < 0 || max_seq_len < 0 || num_splits < 0 ||
-        num_splits > TQ_MAX_SPLITS || !(v_threshold >= 0.f && v_threshold < 1.f) || (mods && (!mods_ok(*mods) || max_seq_len > kMaxListedLen)))
+        num_splits > TQ_MAX_SPLITS || !(v_threshold >= 0.f && v_threshold < 1.f) ||
+        (mods && (!mods_ok(*mods) || max_seq_len > kMaxListedLen)))
         return TQ_ERR_INVALID_ARG;
     if (num_q_heads / num_kv_heads > kMaxGroup) return TQ_ERR_UNSUPPORTED;
     if (batch == 0) return TQ_OK;
@@ -476,10 +477,13 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
     const bool soa = is_soa(preset);
     const int G = num_q_heads / num_kv_heads;
     const int S = num_splits ? num_splits
-                  : mods ? pick_scored_splits(L, soa, batch, num_q_heads, num_kv_heads, max_seq_len, mods->window, mods->prefix)
-                         : pick_splits(L, soa, batch, num_q_heads, num_kv_heads, max_seq_len);
+                  : mods     ? pick_scored_splits(L, soa, batch, num_q_heads, num_kv_heads, max_seq_len,
+                                                  mods->window, mods->prefix)
+                             : pick_splits(L, soa, batch, num_q_heads, num_kv_heads, max_seq_len);
     ScoredLayout lay = {};
-    if (mods) lay = scored_layout(batch, num_q_heads, num_kv_heads, S, max_seq_len, mods->window, mods->prefix, wout != nullptr);
+    if (mods)
+        lay = scored_layout(batch, num_q_heads, num_kv_heads, S, max_seq_len, mods->window, mods->prefix,
+                            wout != nullptr);
     if (workspace_bytes < (mods ? lay.bytes : tq_decode_workspace_bytes(batch, num_q_heads, S, head_dim)))
         return TQ_ERR_WORKSPACE;
     if (wout &&
@@ -548,8 +552,8 @@ int decode_impl(int preset, int head_dim, int batch, int num_q_heads, int num_kv
                            : out_dtype == TQ_F16 ? launch_stage2<__half>(a, mods != nullptr, st)
                                                  : launch_stage2<__nv_bfloat16>(a, mods != nullptr, st);
     if (e2 != cudaSuccess) return TQ_ERR_CUDA;
-    if (wout && launch_weights(a.mods, seq_lens, a.lse, wout->acc, wout->stride_b, wout->stride_h, num_kv_heads, G, st) !=
-                    cudaSuccess)
+    if (wout && launch_weights(a.mods, seq_lens, a.lse, wout->acc, wout->stride_b, wout->stride_h, num_kv_heads, G,
+                               st) != cudaSuccess)
         return TQ_ERR_CUDA;
     return TQ_OK;
 }

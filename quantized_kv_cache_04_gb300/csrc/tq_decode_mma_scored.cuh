@@ -13,9 +13,10 @@
 //   - the value sum about the middle code.
 // Bound, like the plain kernel, by instruction issue and shared-memory lookups for
 // 2- to 4-bit keys, by the copies for FP8 keys: 4 to 9% above the plain decode of
-// the same tokens (4 sequences of 65536 tokens, 8 kv heads, 32 query heads: k8v4
-// 76 us = 0.80 of the copy bandwidth, k3v4 94 us = 0.39; k3v4 at 64 query heads
-// 123 us).
+// the same tokens, up to 15% for groups of 8 (4 sequences of 65536 tokens, 8 kv
+// heads, capped; plain in brackets: 32 query heads k8v4 74 us (75) = 0.82 of the
+// copy bandwidth, k3v4 92 (85) = 0.40, 4bit 101 (94), 3bit 99 (93); 64 query
+// heads 96 (84), 122 (106), 130 (117), 131 (120)).
 // Modes are instantiations, not branches: a branch between the scores and the
 // softmax ends the block in which the compiler overlaps a tile's loads, lookups
 // and MMAs.  The bias is always added (a slope of 0).
@@ -632,22 +633,17 @@ __global__ void __launch_bounds__(512) scored_mma_kernel(const __grid_constant__
         return -1;
     };
     // Misalignment of the warp's key and value loads: FP8 keys are read as
-    // aligned words and their values start aligned.  3-bit keys with 3-bit
-    // values run an instantiation per (key, value) misalignment, picked per
-    // warp (4.7% faster on 256K contexts); the other presets test it in the
-    // loop (separate instantiations cost them instruction-cache misses).
+    // aligned words and their values start aligned; the others test it in the
+    // loop (instances per misalignment, which the plain kernel has for 3-bit keys
+    // with 3-bit values, spill here: groups of 8 151 -> 131 us without them, 4 sequences
+    // of 65536 tokens).
     using M0 = std::integral_constant<int, 0>;
-    using M2 = std::integral_constant<int, 2>;
     using MR = std::integral_constant<int, -1>;
+    using ML = std::integral_constant<int, -2>;
     auto run_mis = [&](auto lo_tag) {
-        if constexpr (LAY == kHalfRows) {
-            using ML = std::integral_constant<int, -2>;
-            return run(lo_tag, ML{}, ML{});
-        } else if constexpr (KMODE == 8) return run(lo_tag, M0{}, M0{});
-        else if constexpr (KMODE == 3 && VBITS == 3) {
-            if (kmis == 0) return vmis == 0 ? run(lo_tag, M0{}, M0{}) : run(lo_tag, M0{}, M2{});
-            else           return vmis == 0 ? run(lo_tag, M2{}, M0{}) : run(lo_tag, M2{}, M2{});
-        } else return run(lo_tag, MR{}, MR{});
+        if constexpr (LAY == kHalfRows) return run(lo_tag, ML{}, ML{});
+        else if constexpr (KMODE == 8)  return run(lo_tag, M0{}, M0{});
+        else                            return run(lo_tag, MR{}, MR{});
     };
     int failed_at;
     if constexpr (KMODE == 2) failed_at = key_lo ? run_mis(std::true_type{}) : run_mis(std::false_type{});

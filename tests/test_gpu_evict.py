@@ -252,3 +252,24 @@ def test_decode_evict_decode(orc, preset, Hk, G):
     torch.cuda.synchronize()
     for a, x in zip(first, (c.cache, acc, out, lse, keep)):
         assert torch.equal(a, x)
+
+
+def test_evict_of_the_cache_object():
+    """TQCache.evict makes its own index and length buffers, and asks for them with a stream of the caller's."""
+    rng = np.random.default_rng(21)
+    lens, Hk, bs, budget = [100, 30], 2, 16, 40
+    cache, bt = _paged(rng, 2, lens, Hk, bs)
+    c = tq.TQCache("turboquant_k3v4_nc", cache.shape[0], bs, Hk)
+    c.cache.copy_(torch.from_numpy(cache))
+    acc = rng.random((2, Hk, 112)).astype(np.float32)
+    accd, sl = torch.from_numpy(acc).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        c.evict(accd, torch.from_numpy(bt).cuda(), sl, 112, budget, stream=torch.cuda.Stream())
+    keep, new = c.evict(accd, torch.from_numpy(bt).cuda(), sl, 112, budget, prefix=3, recent=5)
+    rk, rn = select_ref(acc, lens, budget, 3, 5)
+    want, wacc = compact_ref(cache, bt, rk, lens, bs, acc)
+    assert np.array_equal(keep.cpu().numpy(), rk) and np.array_equal(new.cpu().numpy(), rn)
+    assert np.array_equal(c.cache.cpu().numpy(), want) and np.array_equal(accd.cpu().numpy(), wacc)
+    # the lengths in place of the old ones are refused: they are read while the new ones are written
+    with pytest.raises(tq.TQError):
+        c.evict(accd, torch.from_numpy(bt).cuda(), sl, 112, budget, keep=keep, new_lens=sl)

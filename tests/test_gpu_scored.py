@@ -279,6 +279,31 @@ def test_other_stream_and_graphs(orc):
         assert torch.equal(a, three)
 
 
+def test_two_streams_at_once(orc):
+    """Calls that overlap on the GPU, each with a workspace and sums of its own, over one cache."""
+    pb, q, d = _simple(orc, 1, 8, 8, 32, [900, 411, 0])
+    q = q.cuda()
+    kws = [dict(softcap=15.0), dict(window=333, prefix=2)]
+    want = []
+    for kw in kws:
+        a = torch.zeros((3, 8, 900), device="cuda")
+        want.append((*call(1, q, d, 8, 32, 900, acc=a, **kw), a))
+    streams = [torch.cuda.Stream() for _ in kws]
+    n = max(tq.scored_workspace_bytes(1, 3, 64, 8, 900, kw.get("window", 0), kw.get("prefix", 0), True) for kw in kws)
+    bufs = [(torch.empty_like(want[0][0]), torch.empty_like(want[0][1]), torch.empty(n, dtype=torch.uint8, device="cuda"),
+             torch.zeros_like(want[0][2])) for _ in kws]
+    torch.cuda.synchronize()
+    for rep in range(20):
+        for s, kw, (out, lse, ws, acc) in zip(streams, kws, bufs):
+            with torch.cuda.stream(s):
+                acc.zero_()
+            tq.decode_attention_weights(1, q, d["cache"], d["bt"], d["sl"], 900, 8, 32, d["signs"], d["cent"], out, lse,
+                                        ws, acc, stream=s, **kw)
+    torch.cuda.synchronize()
+    for (o, l, a), (out, lse, _, acc) in zip(want, bufs):
+        assert torch.equal(o, out) and torch.equal(l, lse) and torch.equal(a, acc)
+
+
 def test_many_splits_and_long_context(orc):
     """A long sequence over many splits: every split count gives the same attention."""
     rng = np.random.default_rng(3)
