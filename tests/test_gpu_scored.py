@@ -279,6 +279,32 @@ def test_other_stream_and_graphs(orc):
         assert torch.equal(a, three)
 
 
+@pytest.mark.parametrize("preset,Hk", [(0, 8), (2, 8), (2, 3), (1, 16)])
+def test_cache_past_4_gib(preset, Hk):
+    """Pages whose byte offsets pass 32 bits give what the same pages give in a small cache."""
+    bs, n = 128, 600
+    slot = tq.tq_get_layout(preset)["slot_size_aligned"]
+    nb = (9 << 29) // (bs * Hk * slot) + 1           # about 4.5 GiB
+    rng = np.random.default_rng(preset)
+    c = tq.TQCache(preset, 5, bs, Hk)
+    kv = torch.from_numpy(rng.normal(size=(2, 640, Hk, 128))).half().cuda()
+    c.store(kv[0], kv[1], torch.arange(640, device="cuda"))
+    big = torch.empty((nb,) + c.cache.shape[1:], dtype=torch.uint8, device="cuda")
+    pages = [nb - 1, 0, nb - 2, nb // 2, nb - 7]
+    for i, p in enumerate(pages):
+        big[p] = c.cache[i]
+    q = torch.from_numpy(rng.normal(size=(1, 4 * Hk, 128))).half().cuda()
+    sl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    d = dict(sl=sl, signs=c.signs, cent=c.centroids)
+    got = []
+    for cache, table in ((c.cache, [0, 1, 2, 3, 4]), (big, pages)):
+        acc = torch.zeros((1, Hk, n), device="cuda")
+        bt = torch.tensor([table], dtype=torch.int32, device="cuda")
+        got.append((*call(preset, q, dict(d, cache=cache, bt=bt), Hk, bs, n, acc=acc, softcap=20.0), acc))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_two_streams_at_once(orc):
     """Calls that overlap on the GPU, each with a workspace and sums of its own, over one cache."""
     pb, q, d = _simple(orc, 1, 8, 8, 32, [900, 411, 0])
