@@ -338,8 +338,9 @@ int tq_decode_scored_pick_splits(int preset, int head_dim, int batch, int num_q_
  * partials and where each sequence's lie.  0 for sizes out of range. */
 size_t tq_decode_scored_workspace_bytes(int batch, int num_q_heads, int num_splits, int head_dim);
 
-/* tq_decode_attention with score modifiers; mods NULL (or all zero) is
- * tq_decode_attention exactly (also in the workspace it needs).  num_splits = 0
+/* tq_decode_attention with score modifiers; with mods NULL (or all zero) the
+ * plain decode: tq_decode_attention exactly where that runs on tensor cores
+ * (tq_decode_kernel_kind 1), else the same to rounding.  num_splits = 0
  * picks as tq_decode_scored_pick_splits does.  The splits share the 32-token
  * tiles that hold visible tokens: batch * num_splits splits of one size, given
  * out to the sequences by their visible lengths (batches above 512 sequences:

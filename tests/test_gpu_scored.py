@@ -146,6 +146,23 @@ def test_no_modifier_is_the_plain_decode(orc, preset):
     assert (a - c).abs().max() <= 2e-5 and (la - lc).abs().max() <= LSE_ABS
 
 
+@pytest.mark.parametrize("preset,Hk,soa", [(2, 3, False), (4, 1, False), (3, 5, True), (0, 3, True)])
+def test_no_modifier_where_the_plain_decode_is_on_cuda_cores(orc, preset, Hk, soa):
+    seq_lens = [200, 77, 0]
+    assert tq.tq_decode_kernel_kind(preset | (tq.TQ_LAYOUT_SOA if soa else 0), 128, 4 * Hk, Hk) == 0
+    pb, q, d = _simple(orc, preset, 4, Hk, 16, seq_lens)
+    if soa:
+        d = device_problem(pb, preset, seq_lens, aos_to_soa(orc, preset, pb["cache"]))
+        preset |= tq.TQ_LAYOUT_SOA
+    out, lse = call(preset, q.cuda(), d, Hk, 16, 200)
+    want, wl = torch.empty_like(out), torch.empty_like(lse)
+    ws = torch.empty(tq.tq_decode_workspace_bytes(3, 4 * Hk, 2), dtype=torch.uint8, device="cuda")
+    tq.decode_attention(preset, q.cuda(), d["cache"], d["bt"], d["sl"], 200, Hk, 16, d["signs"], d["cent"], want, wl, ws,
+                        num_splits=2)
+    assert (out - want).abs().max() <= 2e-5
+    assert torch.equal(lse.isneginf(), wl.isneginf()) and (lse - wl).nan_to_num(0.0).abs().max() <= LSE_ABS
+
+
 @pytest.mark.parametrize("preset,Hk", [(0, 8), (2, 8), (2, 3), (4, 1)])
 @pytest.mark.parametrize("bs", [16, 64])
 def test_pages_of_hidden_tokens_are_never_looked_up(orc, preset, Hk, bs):
