@@ -418,7 +418,7 @@ int tq_evict_select(int batch, int num_kv_heads, const float* acc, long long acc
  * distances of alibi_slopes, windows and document starts count in the shortened
  * sequence.
  * keep: as tq_evict_select writes it for these seq_lens (the lengths before the
- * eviction): ascending, so keep[i] >= i.  An entry outside [0, L), or one whose
+ * eviction) and this max_seq_len: ascending, so keep[i] >= i.  An entry outside [0, L), or one whose
  * page or whose destination's page lies outside [0, num_blocks), moves nothing;
  * entries that do not ascend leave unspecified contents in that sequence's own
  * slots.  Pages must belong to one sequence each (a shared page would be moved

@@ -109,5 +109,5 @@ class TQCache:
             new_lens = torch.empty((B,), dtype=torch.int32, device=self.cache.device)
         evict_select(acc, seq_lens, max_seq_len, budget, keep, new_lens, prefix, recent, stream)
         evict_compact(self.preset, keep, seq_lens, self.cache, block_table, self.num_kv_heads, self.block_size,
-                      acc, stream)
+                      acc, stream, max_seq_len)
         return keep, new_lens

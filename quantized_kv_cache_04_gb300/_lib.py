@@ -503,10 +503,11 @@ def evict_select(acc, seq_lens, max_seq_len: int, budget: int, keep, new_lens, p
 
 
 def evict_compact(preset: int, keep, seq_lens, kv_cache, block_table, num_kv_heads: int, block_size: int, acc=None,
-                  stream=None) -> None:
+                  stream=None, max_seq_len: int | None = None) -> None:
     """tq_evict_compact on torch tensors: the slots keep (int32 (B, Hk, budget)) names move to the front of their
     sequences in kv_cache, and the running sums acc (float32 (B, Hk, T)) with them.  seq_lens: the lengths
-    before the eviction; sequences longer than the table or acc covers are left alone."""
+    before the eviction; sequences longer than max_seq_len (that of evict_select), or than the table or acc
+    covers, are left alone."""
     fn, dt = "evict_compact", _dtypes()
     i32 = dt["i32"]
     _need(isinstance(kv_cache, dt["tensor"]) and kv_cache.is_cuda, fn, "kv_cache is not a tensor of a GPU")
@@ -529,6 +530,8 @@ def evict_compact(preset: int, keep, seq_lens, kv_cache, block_table, num_kv_hea
         _on(keep, dev, (i32,), (B, num_kv_heads, None), fn, "keep")
         _on(seq_lens, dev, (i32,), (B,), fn, "seq_lens")
     max_len, budget = min(block_table.shape[1] * block_size, 1 << 30), keep.shape[2]
+    if max_seq_len is not None:
+        max_len = min(max_len, int(max_seq_len))
     a = (None, 0, 0)
     if acc is not None:
         if not _acc_ok(acc, dev, B, num_kv_heads):

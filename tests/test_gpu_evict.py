@@ -270,6 +270,14 @@ def test_evict_of_the_cache_object():
     want, wacc = compact_ref(cache, bt, rk, lens, bs, acc)
     assert np.array_equal(keep.cpu().numpy(), rk) and np.array_equal(new.cpu().numpy(), rn)
     assert np.array_equal(c.cache.cpu().numpy(), want) and np.array_equal(accd.cpu().numpy(), wacc)
+    # a sequence longer than max_seq_len is left alone, slots, sums and length
+    c.cache.copy_(torch.from_numpy(cache))
+    accd = torch.from_numpy(acc).cuda()
+    keep, new = c.evict(accd, torch.from_numpy(bt).cuda(), sl, 99, 20)
+    rk, _ = select_ref(acc, [0, 30], 20, 0, 0)
+    want, wacc = compact_ref(cache, bt, rk, [0, 30], bs, acc)
+    assert new.tolist() == [100, 20] and (keep[0] == -1).all()
+    assert np.array_equal(c.cache.cpu().numpy(), want) and np.array_equal(accd.cpu().numpy(), wacc)
     # the lengths in place of the old ones are refused: they are read while the new ones are written
     with pytest.raises(tq.TQError):
-        c.evict(accd, torch.from_numpy(bt).cuda(), sl, 112, budget, keep=keep, new_lens=sl)
+        c.evict(accd, torch.from_numpy(bt).cuda(), sl, 112, 20, keep=keep, new_lens=sl)
